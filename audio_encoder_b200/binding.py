@@ -33,8 +33,12 @@ EXPORTED = [
     "moss_enc_nvf4_quant_weights",
     "moss_enc_selftest_gelu",
     "moss_enc_selftest_timeout",
+    "moss_enc_gemv_q4", "moss_enc_kv_append", "moss_enc_paged_refusal",
+    "moss_enc_paged_attn_workspace", "moss_enc_paged_attn",
 ]
 WEIGHTS_4BIT = 4
+GEMV_MAX_ROWS = 32
+KV_BF16, KV_F16, KV_E4M3 = 0, 1, 2
 STATIC_MAX_CLIPS = 64
 
 
@@ -58,6 +62,30 @@ class KernelStat(ctypes.Structure):
 class Clip(ctypes.Structure):
     _fields_ = [("pcm", ctypes.c_void_p), ("n_samples", ctypes.c_int64), ("begin", ctypes.c_int64),
                 ("end", ctypes.c_int64), ("log_max", ctypes.c_void_p)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("stride_page", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("n_seqs", ctypes.c_int), ("pages_per_seq", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class KVRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("positions", ctypes.c_void_p), ("seqs", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("n_rows", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("rotary", ctypes.c_int), ("interleaved", ctypes.c_int)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("n_q_heads", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("max_len", ctypes.c_int),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 _lib = None
@@ -135,6 +163,16 @@ def lib():
         L.moss_enc_nvf4_quant_weights.argtypes = [vp, i32, i32, i32, vp, vp, vp]
         L.moss_enc_logmel_static.restype = i32
         L.moss_enc_logmel_static.argtypes = [ctypes.POINTER(Clip), i32, ctypes.POINTER(vp), vp, vp]
+        L.moss_enc_gemv_q4.restype = i32
+        L.moss_enc_gemv_q4.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32]
+        L.moss_enc_kv_append.restype = i32
+        L.moss_enc_kv_append.argtypes = [vp, ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVRows)]
+        L.moss_enc_paged_attn_workspace.restype = i64
+        L.moss_enc_paged_attn_workspace.argtypes = [vp, ctypes.POINTER(KVCacheDesc), i32, i32]
+        L.moss_enc_paged_refusal.restype = ctypes.c_char_p
+        L.moss_enc_paged_refusal.argtypes = [ctypes.POINTER(KVCacheDesc), ctypes.POINTER(KVRows), ctypes.POINTER(Attn)]
+        L.moss_enc_paged_attn.restype = i32
+        L.moss_enc_paged_attn.argtypes = [vp, ctypes.POINTER(KVCacheDesc), ctypes.POINTER(Attn)]
         _lib = L
     return _lib
 
@@ -180,6 +218,47 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
 
+class KVCache:
+    """A paged cache in the caller's tensors, described once for many calls.
+
+    k, v: [n_pages][page_size][n_kv_heads][head_dim] bf16, f16 or
+    float8_e4m3fn; any strides that keep a head's values together and are
+    multiples of 16 bytes, the same for both (pages that hold
+    [n_kv_heads][page_size] are given as a transposed view).  page_table: int32
+    [n_seqs][pages_per_seq].  An e4m3 cache holds keys / k_scale and values /
+    v_scale.  The tensors are kept alive; their contents may change between
+    calls.
+    """
+
+    def __init__(self, k, v, page_table, k_scale: float = 1.0, v_scale: float = 1.0):
+        import torch
+        types = {torch.bfloat16: KV_BF16, torch.float16: KV_F16, torch.float8_e4m3fn: KV_E4M3}
+        if k.dtype not in types or v.dtype != k.dtype or k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v: [n_pages][page_size][n_kv_heads][head_dim], both bf16, f16 or float8_e4m3fn")
+        if page_table.dtype != torch.int32 or page_table.dim() != 2 or not 0 < page_table.shape[1]:
+            raise ValueError("page_table: int32 [n_seqs][pages_per_seq]")
+        if not (k.is_cuda and k.device == v.device == page_table.device):
+            raise ValueError("k, v and page_table must be on one CUDA device")
+        n_pages, page, heads, dim = k.shape
+        # the stride of a dimension of one element says nothing: any will do
+        strides = [dim if n == 1 else s for n, s in zip(k.shape, k.stride())]
+        if strides != [dim if n == 1 else s for n, s in zip(v.shape, v.stride())] or \
+                (dim != 1 and (k.stride(3) != 1 or v.stride(3) != 1)):
+            raise ValueError("k and v must have the same strides and each head's values together")
+        table_stride = page_table.stride(0) if page_table.shape[0] > 1 else page_table.shape[1]
+        if page_table.shape[1] > 1 and page_table.stride(1) != 1:
+            raise ValueError("a row of page_table must be contiguous")
+        self.k, self.v, self.page_table = k, v, page_table
+        self.device, self.dtype, self.types = k.device, k.dtype, types
+        self.n_seqs, self.n_kv_heads, self.head_dim = page_table.shape[0], heads, dim
+        self.rows_dtypes = (torch.bfloat16, torch.float16) if types[k.dtype] == KV_E4M3 else (k.dtype,)
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), table_stride, strides[0], strides[1],
+                                strides[2], page_table.shape[0], page_table.shape[1], n_pages, page, heads, dim,
+                                types[k.dtype], float(k_scale), float(v_scale))
+        self.ref = ctypes.byref(self.desc)
+        self.workspaces = {}  # bytes by (query heads, bound on the lengths)
+
+
 class Encoder:
     """One moss_enc handle on the current CUDA device.
 
@@ -211,6 +290,7 @@ class Encoder:
         if st != OK:
             raise MossEncError(st, "create failed")
         self.h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if getattr(self, "h", None):
@@ -293,6 +373,155 @@ class Encoder:
                 or sfa.numel() < (M + 127) // 128 * 20 * 512 or g.numel() < M):
             raise ValueError("x [M][1280] fp32, codes [M][640], sfa ceil(M/128)*20*512 bytes, g [M]")
         self._check(lib().moss_enc_nvf4_quant_rows(self.h, _ptr(x), _ptr(codes), _ptr(sfa), _ptr(g), M))
+
+    def _on_stream(self, shape, dtype, device):
+        """A new tensor whose memory belongs to the handle's stream."""
+        torch = self.torch
+        if torch.cuda.current_stream(device) == self.stream:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def gemv_q4(self, x, Bq, Bs, bias=None, out=None, epilogue: int = 0):
+        """out = epi(x @ B.T + bias) for 1..32 rows x [M][K] bf16 and B as 4-bit
+        codes Bq [N][K/2] (uint8, even k in the low nibble, code q + 8) with
+        group scales Bs [K/128][N] fp32; bias [N] fp32 or None.  Epilogues 0
+        (bf16), 1 (GELU, bf16), 2 (fp32, out +=: give out) and 5 (fp32)."""
+        torch = self.torch
+        if x.dim() != 2 or Bq.dim() != 2 or Bs.dim() != 2:
+            raise ValueError("x [M][K], Bq [N][K/2], Bs [K/128][N]")
+        M, K = x.shape
+        N = Bq.shape[0]
+        dt = torch.bfloat16 if epilogue in (0, 1) else torch.float32
+        if (x.dtype != torch.bfloat16 or Bq.dtype != torch.uint8 or Bs.dtype != torch.float32 or Bq.shape[1] * 2 != K
+                or K % 128 or tuple(Bs.shape) != (K // 128, N)
+                or not (x.is_contiguous() and Bq.is_contiguous() and Bs.is_contiguous())):
+            raise ValueError("x [M][K] bf16, Bq [N][K/2] uint8, Bs [K/128][N] fp32, contiguous, K a multiple of 128")
+        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()
+                                 or bias.device != x.device):
+            raise ValueError("bias [N] fp32")
+        if out is None:
+            if epilogue == 2:
+                raise ValueError("epilogue 2 adds to out")
+            out = self._on_stream((M, N), dt, x.device)
+        elif out.dtype != dt or tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != x.device:
+            raise ValueError("out [M][N], contiguous, bf16 (epilogues 0, 1) or fp32 (2, 5)")
+        if not x.is_cuda or Bq.device != x.device or Bs.device != x.device:
+            raise ValueError("x, Bq, Bs, bias and out must be on the handle's CUDA device")
+        self._device(x.device)
+        self._check(lib().moss_enc_gemv_q4(self.h, x.data_ptr(), Bq.data_ptr(), Bs.data_ptr(),
+                                           None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K,
+                                           int(epilogue)))
+        return out
+
+    def _device(self, device):
+        if device != self.device:
+            raise ValueError(f"the handle is on {self.device}, the tensors on {device}")
+
+    @staticmethod
+    def _heads(x, rows, heads, dim, dtypes, what):
+        """Row stride of x [rows][heads][dim] whose rows are whole."""
+        if x.dtype not in dtypes or x.dim() != 3 or x.shape[0] != rows or x.shape[2] != dim or \
+                (heads is not None and x.shape[1] != heads):
+            raise ValueError(f"{what}: [rows][heads][head_dim] of the cache's type (bf16 or f16 with an e4m3 cache)")
+        s = x.stride()
+        if s[2] != 1 or (x.shape[1] > 1 and s[1] != dim):
+            raise ValueError(f"{what}: the heads of a row must lie next to one another")
+        return s[0] if rows > 1 else x.shape[1] * dim
+
+    def kv_append(self, cache, k, v, positions, seqs=None, q=None, q_out=None, inv_freq=None, interleaved=False):
+        """Append rows to a KVCache: k, v [rows][n_kv_heads][head_dim], row r
+        at position positions[r] (int32) of sequence seqs[r] (int32; None: row
+        r is sequence r's; negative: a padding row, skipped).  With inv_freq
+        (fp64 [r / 2]) the first r dims of keys and queries turn by positions *
+        inv_freq, in pairs (i, i + r/2) or, interleaved, (2i, 2i + 1).  q
+        [rows][heads][head_dim] is turned into q_out (made here when None; may
+        be q).  Returns q_out."""
+        torch = self.torch
+        rows, dim = k.shape[0], cache.head_dim
+        types = cache.rows_dtypes if k.dtype in cache.rows_dtypes else ()
+        dt = (k.dtype,) if types else ()
+        ks = self._heads(k, rows, cache.n_kv_heads, dim, dt, "k")
+        vs = self._heads(v, rows, cache.n_kv_heads, dim, dt, "v")
+        dev = cache.device
+        qs = qos = hq = 0
+        if q is not None:
+            qs = self._heads(q, rows, None, dim, dt, "q")
+            hq = q.shape[1]
+            if q_out is None:
+                q_out = self._on_stream((rows, hq, dim), q.dtype, dev)
+            qos = self._heads(q_out, rows, hq, dim, dt, "q_out")
+            if q.device != dev or q_out.device != dev:
+                raise ValueError("q and q_out must be on the cache's device")
+        elif q_out is not None:
+            raise ValueError("q_out needs q")
+        rotary = 0
+        if inv_freq is not None:
+            if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.device != dev:
+                raise ValueError("inv_freq: fp64 [r / 2], contiguous")
+            rotary = 2 * inv_freq.shape[0]
+        if positions.dtype != torch.int32 or positions.shape != (rows,) or not positions.is_contiguous():
+            raise ValueError("positions: int32 [rows]")
+        if seqs is not None and (seqs.dtype != torch.int32 or seqs.shape != (rows,) or not seqs.is_contiguous()
+                                 or seqs.device != dev):
+            raise ValueError("seqs: int32 [rows]")
+        if k.device != dev or v.device != dev or positions.device != dev:
+            raise ValueError("k, v and positions must be on the cache's device")
+        self._device(dev)
+        r = KVRows(k.data_ptr(), v.data_ptr(), q.data_ptr() if hq else None, q_out.data_ptr() if hq else None, ks, vs,
+                   qs, qos, positions.data_ptr(), None if seqs is None else seqs.data_ptr(),
+                   inv_freq.data_ptr() if rotary else None, rows, hq, cache.types[k.dtype], rotary,
+                   1 if interleaved else 0)
+        self._check(lib().moss_enc_kv_append(self.h, cache.ref, ctypes.byref(r)))
+        return q_out
+
+    def paged_attn(self, cache, q, lengths, scale=None, out=None, lse=None, return_lse=False, max_len: int = 0,
+                   workspace=None):
+        """One new token per sequence of a KVCache: q [n_seqs][heads][head_dim]
+        attends positions 0 .. lengths - 1 (int32 [n_seqs]) of its sequence;
+        scale defaults to 1 / sqrt(head_dim).  max_len: a known bound on the
+        lengths (0: what the page table holds).  Returns out [n_seqs][heads]
+        [head_dim], and the fp32 log-sum-exp [n_seqs][heads] with return_lse.
+        workspace: uint8, paged_attn_workspace() bytes (made here when None)."""
+        torch = self.torch
+        dev, dim, n = cache.device, cache.head_dim, cache.n_seqs
+        dt = (q.dtype,) if q.dtype in cache.rows_dtypes else ()
+        qs = self._heads(q, n, None, dim, dt, "q")
+        hq = q.shape[1]
+        if out is None:
+            out = self._on_stream((n, hq, dim), q.dtype, dev)
+        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+            raise ValueError("out: contiguous, of q's shape and type")
+        if lse is None:
+            if return_lse:
+                lse = self._on_stream((n, hq), torch.float32, dev)
+        elif lse.dtype != torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError("lse: fp32 [n_seqs][heads]")
+        if lengths.dtype != torch.int32 or lengths.shape != (n,) or not lengths.is_contiguous() or lengths.device != dev \
+                or q.device != dev:
+            raise ValueError("lengths: int32 [n_seqs], on the cache's device")
+        self._device(dev)
+        need = self.paged_attn_workspace(cache, hq, max_len)
+        if workspace is None:
+            if need:
+                workspace = self._on_stream((need,), torch.uint8, dev)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+            raise ValueError("workspace: uint8, contiguous, on the cache's device")
+        a = Attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), lengths.data_ptr(), qs, hq,
+                 cache.types[q.dtype], dim ** -0.5 if scale is None else scale, int(max_len),
+                 None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+        self._check(lib().moss_enc_paged_attn(self.h, cache.ref, ctypes.byref(a)))
+        return (out, lse) if return_lse else out
+
+    def paged_attn_workspace(self, cache, heads: int, max_len: int = 0) -> int:
+        """Bytes that paged_attn needs as workspace."""
+        key = (heads, int(max_len))
+        if key not in cache.workspaces:
+            need = int(lib().moss_enc_paged_attn_workspace(self.h, cache.ref, heads, int(max_len)))
+            if need < 0:
+                raise MossEncError(1, "paged_attn: cache, heads or max_len refused")
+            cache.workspaces[key] = need
+        return cache.workspaces[key]
 
     def selftest_timeout(self, limit_ms: int = 50):
         self._check(lib().moss_enc_selftest_timeout(self.h, int(limit_ms)))

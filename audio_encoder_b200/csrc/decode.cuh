@@ -1,0 +1,596 @@
+// The attention side of one decoding step: keys and values appended to a
+// paged cache with the position rotation on the way, and the attention of one
+// new token per sequence over that cache.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <type_traits>
+
+#include "attn.cuh"
+#include "common.cuh"
+#include "gemv.cuh"
+
+namespace moss {
+
+enum : int { KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2 };
+
+// Device error word bits of the paged calls (a word of its own in the flag
+// block: the bounded waits read the timeout word).
+enum : int { DEV_ERR_PAGE = 1 };
+
+// The caller's pages (moss_enc_kv_cache), with the page size as a shift.
+struct PagedKV {
+    uint8_t *k, *v;
+    const int *table;
+    long long table_stride;
+    long long stride_page, stride_token, stride_head;  // bytes
+    int n_seqs, pages_per_seq, n_pages, page_shift, hkv, dim;
+    float k_scale, v_scale;
+    int *flag;
+
+    // Byte offset of position pos (its page already looked up).
+    __device__ __forceinline__ long long at(int page, int pos) const
+    {
+        return page * stride_page + (pos & ((1 << page_shift) - 1)) * stride_token;
+    }
+    // The page that holds position pos of sequence s, or -1 with the error
+    // word set when the table names a page that the cache does not have.
+    __device__ __forceinline__ int page_of(int s, int pos) const
+    {
+        const int p = table[s * table_stride + (pos >> page_shift)];
+        if ((unsigned)p < (unsigned)n_pages) return p;
+        atomicOr(flag, DEV_ERR_PAGE);
+        return -1;
+    }
+};
+
+// ------------------------------------------------------------ append
+
+struct AppendArgs {
+    PagedKV c;
+    const uint16_t *k, *v, *q;
+    uint16_t *q_out;
+    long long k_stride, v_stride, q_stride, q_out_stride;  // elements between rows
+    const int *positions, *seqs;
+    const double *inv_freq;
+    int hq, rotary, interleaved;
+    float inv_k_scale, inv_v_scale;
+};
+
+template <typename T>
+__device__ __forceinline__ float2 to_f2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 to_f2<bf16>(uint32_t w)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+template <>
+__device__ __forceinline__ float2 to_f2<__half>(uint32_t w)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t from_f2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t from_f2<bf16>(float x, float y)
+{
+    return pack_bf16x2(x, y);
+}
+template <>
+__device__ __forceinline__ uint32_t from_f2<__half>(float x, float y)
+{
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 f = to_f2<T>(u[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+{
+    return make_uint4(from_f2<T>(x[0], x[1]), from_f2<T>(x[2], x[3]), from_f2<T>(x[4], x[5]), from_f2<T>(x[6], x[7]));
+}
+
+// Eight values as e4m3 (round to nearest even, held at +-448; NaN stays NaN).
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv)
+{
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+        r[i] = lo | (hi << 16);
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// One CTA per row: its angles once, in shared memory, then the row's heads,
+// 16 values a thread: values i .. i+7 and their partners (half a rotated span
+// further, or the next eight when pairs lie side by side).
+//
+// Angles grow with the position, so they are taken in 64 bits, as a fraction
+// of a turn (pos * inv_freq / 2 pi less its nearest whole number), and only
+// that fraction goes to fp32 for the sine and cosine.
+template <typename T, bool E4M3>
+__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
+{
+    __shared__ float2 cs[128];
+    const int row = blockIdx.x, tid = threadIdx.x;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int seq = a.seqs ? a.seqs[row] : row;
+    if (seq < 0) return;  // a padding row: nothing is written
+    const int pos = a.positions[row];
+    int page = -1;
+    if (seq < a.c.n_seqs && pos >= 0 && (pos >> a.c.page_shift) < a.c.pages_per_seq)
+        page = a.c.page_of(seq, pos);
+    else if (tid == 0)
+        atomicOr(a.c.flag, DEV_ERR_PAGE);
+    if (page < 0) return;
+
+    for (int i = tid; i < a.rotary / 2; i += blockDim.x) {
+        const double turns = (double)pos * a.inv_freq[i] * 0.15915494309189533577;
+        const float f = (float)(turns - rint(turns));
+        float s, c;
+        sincospif(2.0f * f, &s, &c);
+        cs[i] = make_float2(c, s);
+    }
+    __syncthreads();
+
+    const int per_head = a.c.dim / 16, rot_items = a.rotary / 16;
+    const int items = (a.hq + 2 * a.c.hkv) * per_head;
+    const long long slot = a.c.at(page, pos);
+    for (int it = tid; it < items; it += blockDim.x) {
+        int h = it / per_head;
+        const int j = it - h * per_head;
+        const uint16_t *src;
+        enum { Q, K, V } what;
+        if (h < a.hq) {
+            what = Q;
+            src = a.q + row * a.q_stride + h * a.c.dim;
+        } else if ((h -= a.hq) < a.c.hkv) {
+            what = K;
+            src = a.k + row * a.k_stride + h * a.c.dim;
+        } else {
+            h -= a.c.hkv;
+            what = V;
+            src = a.v + row * a.v_stride + h * a.c.dim;
+        }
+        int d0 = 16 * j, d1 = d0 + 8;
+        const bool turn = what != V && j < rot_items;
+        if (turn && !a.interleaved) {
+            d0 = 8 * j;
+            d1 = a.rotary / 2 + 8 * j;
+        }
+        float x[8], y[8];
+        unpack8<T>(*reinterpret_cast<const uint4 *>(src + d0), x);
+        unpack8<T>(*reinterpret_cast<const uint4 *>(src + d1), y);
+        if (turn) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float2 e = cs[8 * j + i], f = cs[8 * j + 4 + i];
+                    const float x0 = x[2 * i], x1 = x[2 * i + 1], y0 = y[2 * i], y1 = y[2 * i + 1];
+                    x[2 * i] = x0 * e.x - x1 * e.y;
+                    x[2 * i + 1] = x1 * e.x + x0 * e.y;
+                    y[2 * i] = y0 * f.x - y1 * f.y;
+                    y[2 * i + 1] = y1 * f.x + y0 * f.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float2 e = cs[8 * j + i];
+                    const float x0 = x[i], y0 = y[i];
+                    x[i] = x0 * e.x - y0 * e.y;
+                    y[i] = y0 * e.x + x0 * e.y;
+                }
+            }
+        }
+        if (what == Q) {
+            uint16_t *dst = a.q_out + row * a.q_out_stride + h * a.c.dim;
+            *reinterpret_cast<uint4 *>(dst + d0) = pack8<T>(x);
+            *reinterpret_cast<uint4 *>(dst + d1) = pack8<T>(y);
+        } else {
+            uint8_t *dst = (what == K ? a.c.k : a.c.v) + slot + h * a.c.stride_head;
+            if (E4M3) {
+                const float inv = what == K ? a.inv_k_scale : a.inv_v_scale;
+                *reinterpret_cast<uint2 *>(dst + d0) = pack8_e4m3(x, inv);
+                *reinterpret_cast<uint2 *>(dst + d1) = pack8_e4m3(y, inv);
+            } else {
+                *reinterpret_cast<uint4 *>(dst + 2 * d0) = pack8<T>(x);
+                *reinterpret_cast<uint4 *>(dst + 2 * d1) = pack8<T>(y);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ attention
+
+struct PagedAttnArgs {
+    PagedKV c;
+    const uint16_t *q;   // [n_seqs][hq][dim], rows q_stride elements apart
+    uint16_t *out;       // [n_seqs][hq][dim]
+    float *lse;          // [n_seqs][hq] or null
+    const int *lengths;  // [n_seqs]
+    long long q_stride;
+    int hq, group;       // query heads, query heads per key head
+    int head_groups;     // groups of 8 NT query heads that share a key head
+    float scale_log2;    // scale * log2(e)
+};
+
+__device__ __forceinline__ void mma_16816(bf16, float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    mma_16816_bf16(d, a0, a1, a2, a3, b0, b1);
+}
+__device__ __forceinline__ void mma_16816(__half, float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 matrix of 16-bit values, rows lane / 4, columns 2 (lane % 4) and
+// the next, turned over.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v)
+{
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
+    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+}
+
+__device__ __forceinline__ uint2 ldg_stream8(const void *p)
+{
+    uint2 v;
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+// W words of 16-bit pairs of consecutive dims, from a 16-bit or an e4m3 cache.
+template <bool E4M3, int W>
+__device__ __forceinline__ void load_dims(const uint8_t *p, uint32_t (&w)[W])
+{
+    if constexpr (!E4M3) {
+        static_assert(W == 4, "16 bytes");
+        const uint4 v = ldg_stream16(p);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (W == 4) {
+        const uint2 v = ldg_stream8(p);
+        w[0] = e4m3x2_to_half2(v.x), w[1] = e4m3x2_to_half2(v.x >> 16);
+        w[2] = e4m3x2_to_half2(v.y), w[3] = e4m3x2_to_half2(v.y >> 16);
+    } else {
+        static_assert(W == 8, "16 bytes");
+        const uint4 v = ldg_stream16(p);
+        w[0] = e4m3x2_to_half2(v.x), w[1] = e4m3x2_to_half2(v.x >> 16);
+        w[2] = e4m3x2_to_half2(v.y), w[3] = e4m3x2_to_half2(v.y >> 16);
+        w[4] = e4m3x2_to_half2(v.z), w[5] = e4m3x2_to_half2(v.z >> 16);
+        w[6] = e4m3x2_to_half2(v.w), w[7] = e4m3x2_to_half2(v.w >> 16);
+    }
+}
+
+static constexpr int PA_WARPS = 8;
+static constexpr int PA_TILE = 16 * PA_WARPS;  // positions that a CTA's warps take at once
+
+// What a warp holds of up to 8 NT query heads that share a key head, over the
+// positions it has seen: with s = scale log2(e) q.k, the running maximum m,
+// l = sum 2^(s - m) and o = sum 2^(s - m) v.
+//
+// Keys and values are the A operands, straight from global memory, and the
+// query heads are the 8 columns: S^T = K q^T has 16 positions x 8 heads, its
+// probabilities turn into the B operand of O^T = V^T P^T by two 8 x 8
+// transposes, and nothing passes through shared memory.  Lane (g, t) reads
+// key rows g and g + 8 in 16-byte pieces; which dims share an instruction's k
+// is free as long as q uses the same ones.  It reads its piece g of the value
+// rows 2t, 2t + 1, 2t + 8, 2t + 9 and pairs the rows' 16-bit halves, which
+// gives the V^T operand with the dims in an order that only the store knows.
+//
+// mma.sync rather than tcgen05: a tcgen05 product has 128 rows, and its
+// operands come from shared memory; here 8 columns suffice and the reads of
+// the cache are what bounds the kernel.
+template <typename T, bool E4M3, int D, int NT>
+struct PagedState {
+    static constexpr int KD = E4M3 ? 16 : 8;                 // dims in a lane's piece of a key row
+    static constexpr int KJ = D / (4 * KD);                  // pieces
+    static constexpr int VD = E4M3 && D >= 128 ? 16 : 8;     // dims in a lane's piece of a value row
+    static constexpr int VI = D / (8 * VD);                  // pieces
+    static constexpr int VJ = VD / 2;                        // 16-dim tiles per piece
+    static constexpr int TILES = D / 16;
+    static constexpr int ESZ = E4M3 ? 1 : 2;
+    static constexpr int SLOT = NT * TILES * 4 * 32 + NT * 4 * 32;  // floats of a saved state
+
+    uint32_t q[NT][TILES][2];
+    float o[NT][TILES][4];
+    float m[NT][2], l[NT][2], sc[NT][2];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) o[n][i][j] = 0.0f;
+        }
+    }
+
+    // The query heads as B operands; heads past `heads` are zero.  An e4m3
+    // cache is multiplied in f16: bf16 queries are brought to f16 by a power
+    // of two of the head's own (its largest value to [256, 512)), which the
+    // score's factor takes back, so no query is out of f16's range and what
+    // underflows is 2^-33 of the head's largest.
+    template <typename QT>
+    __device__ __forceinline__ void load_q(const uint16_t *src, int heads, float scale_log2, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const bool live = n * 8 + g < heads;
+            const uint16_t *p = src + (long long)(n * 8 + g) * D;
+            float back = 1.0f;
+            if constexpr (!E4M3) {
+#pragma unroll
+                for (int j = 0; j < KJ; j++) {
+                    const uint4 v = live ? *reinterpret_cast<const uint4 *>(p + KD * (t + 4 * j)) : make_uint4(0, 0, 0, 0);
+                    q[n][2 * j][0] = v.x, q[n][2 * j][1] = v.y, q[n][2 * j + 1][0] = v.z, q[n][2 * j + 1][1] = v.w;
+                }
+            } else {
+                float x[KJ][16];
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < KJ; j++)
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint4 v = live ? *reinterpret_cast<const uint4 *>(p + KD * (t + 4 * j) + 8 * i) : make_uint4(0, 0, 0, 0);
+                        unpack8<QT>(v, *reinterpret_cast<float(*)[8]>(&x[j][8 * i]));
+#pragma unroll
+                        for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[j][8 * i + e]));
+                    }
+                float up = 1.0f;
+                if constexpr (!std::is_same<QT, __half>::value) {
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    if (top > 0.0f && top < INFINITY) {
+                        const int e = min(max(8 - ilogbf(top), -126), 126);
+                        up = ldexpf(1.0f, e);
+                        back = ldexpf(1.0f, -e);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < KJ; j++)
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++)
+                            q[n][4 * j + s][e] = from_f2<__half>(x[j][4 * s + 2 * e] * up, x[j][4 * s + 2 * e + 1] * up);
+            }
+            // the factor of head 2t (and the next), from the lanes that hold its query
+            sc[n][0] = scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 8 * t);
+            sc[n][1] = scale_log2 * __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+        }
+    }
+
+    // Positions p0 .. p0 + 15 (one page; those at or past `end` are masked),
+    // whose keys and values start at kp and vp, rows `stride` bytes apart.
+    __device__ __forceinline__ void step(const uint8_t *kp, const uint8_t *vp, long long stride, int p0, int end, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        const uint8_t *k0 = kp + g * stride + t * 16, *k1 = k0 + 8 * stride;
+        const uint8_t *v0 = vp + 2 * t * stride + g * VD * ESZ;
+        uint32_t ka[KJ][KD / 2], kb[KJ][KD / 2];
+#pragma unroll
+        for (int j = 0; j < KJ; j++) {
+            load_dims<E4M3>(k0 + 64 * j, ka[j]);
+            load_dims<E4M3>(k1 + 64 * j, kb[j]);
+        }
+        uint32_t v[VI][4][VJ];
+#pragma unroll
+        for (int i = 0; i < VI; i++) {
+            load_dims<E4M3>(v0 + i * 8 * VD * ESZ, v[i][0]);
+            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + stride, v[i][1]);
+            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + 8 * stride, v[i][2]);
+            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + 9 * stride, v[i][3]);
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            float s[4] = {};
+#pragma unroll
+            for (int j = 0; j < KJ; j++)
+#pragma unroll
+                for (int e = 0; e < KD / 4; e++)
+                    mma_16816(T(), s, ka[j][2 * e], kb[j][2 * e], ka[j][2 * e + 1], kb[j][2 * e + 1],
+                              q[n][j * (KD / 4) + e][0], q[n][j * (KD / 4) + e][1]);
+            // s: positions g (0, 1) and g + 8 (2, 3), heads 2t and 2t + 1
+            s[0] = p0 + g < end ? s[0] * sc[n][0] : -INFINITY;
+            s[1] = p0 + g < end ? s[1] * sc[n][1] : -INFINITY;
+            s[2] = p0 + g + 8 < end ? s[2] * sc[n][0] : -INFINITY;
+            s[3] = p0 + g + 8 < end ? s[3] * sc[n][1] : -INFINITY;
+            float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, x));
+                t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, x));
+            }
+            if (__any_sync(0xFFFFFFFFu, t0 > m[n][0] || t1 > m[n][1])) {
+                const float n0 = fmaxf(m[n][0], t0), n1 = fmaxf(m[n][1], t1);
+                const float f0 = n0 == -INFINITY ? 1.0f : ex2_approx(m[n][0] - n0);
+                const float f1 = n1 == -INFINITY ? 1.0f : ex2_approx(m[n][1] - n1);
+                m[n][0] = n0, m[n][1] = n1;
+                l[n][0] *= f0, l[n][1] *= f1;
+#pragma unroll
+                for (int i = 0; i < TILES; i++) {
+                    o[n][i][0] *= f0, o[n][i][1] *= f1, o[n][i][2] *= f0, o[n][i][3] *= f1;
+                }
+            }
+            const float b0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], b1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+            s[0] = ex2_approx(s[0] - b0), s[1] = ex2_approx(s[1] - b1);
+            s[2] = ex2_approx(s[2] - b0), s[3] = ex2_approx(s[3] - b1);
+            l[n][0] += s[0] + s[2], l[n][1] += s[1] + s[3];
+            // the probabilities are rounded to the cache's 16-bit type for
+            // the product (half an ulp each, errors that average out over the
+            // positions); their sum keeps 32 bits
+            pb[n][0] = movmatrix(from_f2<T>(s[0], s[1]));
+            pb[n][1] = movmatrix(from_f2<T>(s[2], s[3]));
+        }
+        if (p0 + 16 > end) {
+            // masked rows hold anything: 0 * NaN must not reach the sum
+#pragma unroll
+            for (int r = 0; r < 4; r++)
+                if (p0 + 2 * t + (r & 1) + 4 * (r & 2) >= end)
+#pragma unroll
+                    for (int i = 0; i < VI; i++)
+#pragma unroll
+                        for (int j = 0; j < VJ; j++) v[i][r][j] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < VI; i++)
+#pragma unroll
+            for (int j = 0; j < VJ; j++) {
+                const uint32_t a0 = __byte_perm(v[i][0][j], v[i][1][j], 0x5410), a1 = __byte_perm(v[i][0][j], v[i][1][j], 0x7632);
+                const uint32_t a2 = __byte_perm(v[i][2][j], v[i][3][j], 0x5410), a3 = __byte_perm(v[i][2][j], v[i][3][j], 0x7632);
+#pragma unroll
+                for (int n = 0; n < NT; n++) mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            }
+    }
+
+    // Positions [t0, end) of one key head of sequence s, 16 at a time, by the
+    // CTA's warps in turn.
+    __device__ __forceinline__ void run(const PagedKV &c, int s, int head, int t0, int end, int warp, int lane)
+    {
+        for (int p0 = t0 + 16 * warp; p0 < end; p0 += PA_TILE) {
+            const int page = max(c.page_of(s, p0), 0);
+            const long long off = c.at(page, p0) + head * c.stride_head;
+            step(c.k + off, c.v + off, c.stride_token, p0, end, lane);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                l[n][0] += __shfl_xor_sync(0xFFFFFFFFu, l[n][0], x);
+                l[n][1] += __shfl_xor_sync(0xFFFFFFFFu, l[n][1], x);
+            }
+    }
+
+    __device__ __forceinline__ void save(float *slot, int lane) const
+    {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) slot[((n * TILES + i) * 4 + j) * 32 + lane] = o[n][i][j];
+            float *st = slot + NT * TILES * 128 + n * 128 + lane;
+            st[0] = m[n][0], st[32] = m[n][1], st[64] = l[n][0], st[96] = l[n][1];
+        }
+    }
+
+    // Joins a saved state of other positions: both sides to the larger maximum.
+    __device__ __forceinline__ void join(const float *slot, int lane)
+    {
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            const float *st = slot + NT * TILES * 128 + n * 128 + lane;
+            float fa[2], fb[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float mb = st[32 * e], top = fmaxf(m[n][e], mb);
+                fa[e] = top == -INFINITY ? 1.0f : ex2_approx(m[n][e] - top);
+                fb[e] = top == -INFINITY ? 1.0f : ex2_approx(mb - top);
+                m[n][e] = top;
+                l[n][e] = l[n][e] * fa[e] + st[64 + 32 * e] * fb[e];
+            }
+#pragma unroll
+            for (int i = 0; i < TILES; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    o[n][i][j] = o[n][i][j] * fa[j & 1] + slot[((n * TILES + i) * 4 + j) * 32 + lane] * fb[j & 1];
+        }
+    }
+
+    // The states of the CTA's warps joined into warp 0's, halving the warps
+    // that hold one; slots: PA_WARPS / 2 of them in shared memory.
+    __device__ __forceinline__ void join_warps(float *slots, int warp, int lane)
+    {
+#pragma unroll
+        for (int w = PA_WARPS / 2; w >= 1; w >>= 1) {
+            if (warp >= w && warp < 2 * w) save(slots + (warp - w) * SLOT, lane);
+            __syncthreads();
+            if (warp < w) join(slots + warp * SLOT, lane);
+            __syncthreads();
+        }
+    }
+
+    // out and lse of the heads from `head` on, of which `heads` are live.
+    template <typename QT>
+    __device__ __forceinline__ void store(uint16_t *out, float *lse, int heads, float v_scale, int lane) const
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int h = n * 8 + 2 * t + e;
+                if (h >= heads) continue;
+                const float inv = l[n][e] == 0.0f ? 0.0f : v_scale / l[n][e];
+                uint16_t *dst = out + (long long)h * D;
+#pragma unroll
+                for (int i = 0; i < VI; i++)
+#pragma unroll
+                    for (int j = 0; j < VJ; j++)
+                        *reinterpret_cast<uint32_t *>(dst + i * 8 * VD + g * VD + 2 * j) =
+                            from_f2<QT>(o[n][i * VJ + j][e] * inv, o[n][i * VJ + j][2 + e] * inv);
+                if (lse && g == 0) lse[h] = (m[n][e] + log2f(l[n][e])) * 0.69314718055994531f;
+            }
+    }
+};
+
+// One CTA per (sequence, key head and its group of query heads).
+template <typename T, typename QT, bool E4M3, int D, int NT>
+__global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a)
+{
+    using S = PagedState<T, E4M3, D, NT>;
+    extern __shared__ __align__(16) float pa_slots[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int head = blockIdx.x / a.head_groups, hg = blockIdx.x - head * a.head_groups, s = blockIdx.y;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int cap = a.c.pages_per_seq << a.c.page_shift;
+    int len = a.lengths[s];
+    if (len < 0 || len > cap) {
+        if (tid == 0) atomicOr(a.c.flag, DEV_ERR_PAGE);
+        len = min(max(len, 0), cap);
+    }
+    const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    S st;
+    st.clear();
+    st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
+    st.run(a.c, s, head, 0, len, warp, lane);
+    st.join_warps(pa_slots, warp, lane);
+    if (warp == 0)
+        st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr,
+                              heads, E4M3 ? a.c.v_scale : 1.0f, lane);
+}
+
+}  // namespace moss

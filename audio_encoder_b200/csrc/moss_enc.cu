@@ -19,6 +19,7 @@
 #include "../../include/moss_enc.h"
 #include "attn.cuh"
 #include "common.cuh"
+#include "decode.cuh"
 #include "gemm.cuh"
 #include "mel.cuh"
 #include "norm.cuh"
@@ -34,6 +35,7 @@ constexpr int CHUNK_FRAMES = 800, CHUNK_TOKENS = 100, CHUNK_SAMPLES = 128000, HO
 constexpr int CONV_K = 9 * 512;  // conv2/conv3 patch width: 9 taps x 480 channels padded to 512
 constexpr int CONV_BN = 240;     // conv2/conv3 output channels per pair tile (480 in two)
 constexpr int STEM_GROUP_DEFAULT = 32;
+constexpr int PAGE_FLAG_WORD = 16;  // the paged calls' error word in the flag block (word 0: timed-out waits)
 constexpr int C2_TILES = 50, C3_TILES = 13;  // 128-row tiles per chunk of conv2 (4 t x 32 f) / conv3 (8 t x 16 f)
 
 // A weight matrix kept as 4-bit codes: codes [N][Kq/2] bytes (two per byte,
@@ -1450,12 +1452,15 @@ extern "C" moss_enc_status moss_enc_synchronize(moss_enc *h)
 {
     if (!h) return MOSS_ENC_ERR_INVALID_ARG;
     CUDA_TRY(h, cudaStreamSynchronize(h->stream));
-    int e = 0;
-    CUDA_TRY(h, cudaMemcpy(&e, h->err, sizeof(int), cudaMemcpyDeviceToHost));
-    if (e != 0) {
+    int e[PAGE_FLAG_WORD + 1] = {};
+    CUDA_TRY(h, cudaMemcpy(e, h->err, sizeof(e), cudaMemcpyDeviceToHost));
+    if (e[PAGE_FLAG_WORD] != 0) CUDA_TRY(h, cudaMemset(h->err + PAGE_FLAG_WORD, 0, sizeof(int)));
+    if (e[0] != 0) {
         CUDA_TRY(h, cudaMemset(h->err, 0, sizeof(int)));
         return fail(h, MOSS_ENC_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait timed out");
     }
+    if (e[PAGE_FLAG_WORD] != 0)
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "a sequence, position, length or page lies outside the paged cache");
     return MOSS_ENC_OK;
 }
 
@@ -2548,6 +2553,275 @@ extern "C" moss_enc_status moss_enc_nvf4_quant_rows(moss_enc *h, const float *x,
     CUDA_TRY(h, launch_k(h, nvf4_rows1280_kernel<false>, dim3((M + 7) / 8), dim3(256), 0, x, (const float *)nullptr,
                          (const float *)nullptr, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(sfa), g, M));
     return MOSS_ENC_OK;
+}
+
+// ------------------------------------------------------- one decoding step
+
+namespace {
+// Makes the handle's device current for a launch and puts the caller's back.
+struct OnDevice {
+    int before = -1;
+    explicit OnDevice(const moss_enc *h)
+    {
+        int d = -1;
+        if (cudaGetDevice(&d) == cudaSuccess && d != h->device && cudaSetDevice(h->device) == cudaSuccess) before = d;
+    }
+    ~OnDevice()
+    {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+}  // namespace
+
+static bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs,
+                                            const float *bias, void *out, int M, int N, int K, int epilogue)
+{
+    if (!h) return MOSS_ENC_ERR_INVALID_ARG;
+    if (M < 0 || M > MOSS_ENC_GEMV_MAX_ROWS || N <= 0 || K <= 0 || K % 128 != 0)
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "rows must be 0..32, N >= 1 and K a multiple of 128");
+    if (epilogue != GV_BF16 && epilogue != GV_GELU_BF16 && epilogue != GV_RESID_F32 && epilogue != GV_F32)
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "unsupported epilogue");
+    if (M == 0) return MOSS_ENC_OK;
+    const bool wide = epilogue == GV_RESID_F32 || epilogue == GV_F32;
+    if (!x || !Bq || !Bs || !out || !aligned(x, 16) || !aligned(Bq, 16) || !aligned(Bs, 4) || !aligned(bias, 4) ||
+        !aligned(out, wide ? 4 : 2))
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "x and Bq must be 16-byte aligned, Bs, bias and out to their elements");
+    GemvArgs a{};
+    a.x = static_cast<const bf16 *>(x);
+    a.codes = static_cast<const uint8_t *>(Bq);
+    a.scales = Bs;
+    a.bias = bias;
+    a.out = out;
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.epi = epilogue;
+    OnDevice dev(h);
+    Launch L(h, "gemv_q4", 2.0 * M * N * K, 0.5 * N * (double)K + 4.0 * N * (K / 128) + 2.0 * M * K +
+                                                (epilogue == GV_RESID_F32 ? 8.0 : wide ? 4.0 : 2.0) * M * N);
+    const dim3 grid((N + 15) / 16), block(32 * GV_WARPS);
+    if (M <= 8)
+        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<1>, grid, block, 0, a));
+    else if (M <= 16)
+        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<2>, grid, block, 0, a));
+    else
+        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<4>, grid, block, 0, a));
+    return MOSS_ENC_OK;
+}
+
+// The reasons for which the paged calls refuse their arguments (null: none);
+// no device is touched.
+static const char *cache_refusal(const moss_enc_kv_cache *c)
+{
+    if (!c) return "no cache";
+    if (c->dtype != MOSS_ENC_KV_BF16 && c->dtype != MOSS_ENC_KV_F16 && c->dtype != MOSS_ENC_KV_E4M3)
+        return "unknown cache type";
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return "head_dim must be 64, 128 or 256";
+    if (c->n_seqs < 0 || c->n_kv_heads < 1 || c->n_kv_heads > 65535 || c->n_pages < 1 || c->pages_per_seq < 1)
+        return "n_seqs, n_kv_heads, n_pages or pages_per_seq out of range";
+    if (c->page_size < 16 || (c->page_size & (c->page_size - 1)) != 0) return "page_size must be a power of two, 16 or more";
+    if ((int64_t)c->page_size * c->pages_per_seq > INT32_MAX) return "a sequence's pages hold 2^31 positions or more";
+    if (!c->k || !c->v || (!c->page_table && c->n_seqs > 0) || !aligned(c->k, 16) || !aligned(c->v, 16) ||
+        !aligned(c->page_table, 4))
+        return "k and v must be 16-byte aligned, page_table 4-byte";
+    const int es = c->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2;
+    const int64_t strides[3] = {c->stride_page, c->stride_token, c->stride_head};
+    const int64_t counts[3] = {c->n_pages, c->page_size, c->n_kv_heads};
+    for (int i = 0; i < 3; i++) {
+        if (strides[i] < 0 || strides[i] % (16 / es) != 0) return "strides must be non-negative multiples of 16 bytes";
+        if (strides[i] > (INT64_MAX >> 4) / counts[i]) return "a stride is out of range";
+    }
+    // one page or one head leaves its stride without meaning
+    if ((c->n_kv_heads > 1 && c->stride_head < c->head_dim) || c->stride_token < c->head_dim ||
+        (c->n_pages > 1 && c->stride_page < c->head_dim) || (c->n_seqs > 1 && c->table_stride < c->pages_per_seq))
+        return "strides overlap";
+    if (c->dtype == MOSS_ENC_KV_E4M3 && !(c->k_scale > 0.0f && c->v_scale > 0.0f && std::isfinite(c->k_scale) &&
+                                          std::isfinite(c->v_scale) && std::isfinite(1.0f / c->k_scale) &&
+                                          std::isfinite(1.0f / c->v_scale)))
+        return "k_scale and v_scale must be positive and finite, and their reciprocals too";
+    return nullptr;
+}
+
+// The 16-bit type of rows that meet a cache: its own, or either at an e4m3 one.
+static bool row_type_ok(const moss_enc_kv_cache *c, int dtype)
+{
+    return (dtype == MOSS_ENC_KV_BF16 || dtype == MOSS_ENC_KV_F16) && (c->dtype == MOSS_ENC_KV_E4M3 || c->dtype == dtype);
+}
+
+static const char *rows_refusal(const moss_enc_kv_cache *c, const moss_enc_kv_rows *r)
+{
+    if (r->n_rows < 0 || r->n_q_heads < 0 || r->n_q_heads > 65535) return "n_rows or n_q_heads out of range";
+    if (!row_type_ok(c, r->dtype)) return "rows must be of the cache's 16-bit type (either with an e4m3 cache)";
+    if (r->rotary < 0 || r->rotary > c->head_dim || r->rotary % 16 != 0 || (r->rotary > 0 && !r->inv_freq) ||
+        !aligned(r->inv_freq, 8) || r->interleaved < 0 || r->interleaved > 1)
+        return "rotary must be a multiple of 16 up to head_dim, with inv_freq; interleaved 0 or 1";
+    const int64_t kv_row = (int64_t)c->n_kv_heads * c->head_dim, q_row = (int64_t)r->n_q_heads * c->head_dim;
+    if (r->k_stride % 8 != 0 || r->v_stride % 8 != 0 || r->q_stride % 8 != 0 || r->q_out_stride % 8 != 0)
+        return "row strides must be multiples of 16 bytes";
+    if (r->n_rows > 1 && (r->k_stride < kv_row || r->v_stride < kv_row ||
+                          (r->n_q_heads > 0 && (r->q_stride < q_row || r->q_out_stride < q_row))))
+        return "rows overlap";
+    if (r->n_rows == 0) return nullptr;
+    if (!r->k || !r->v || !r->positions || (r->n_q_heads > 0 && (!r->q || !r->q_out))) return "a pointer is missing";
+    for (const void *p : {r->k, r->v, r->q, static_cast<const void *>(r->q_out)})
+        if (!aligned(p, 16)) return "k, v, q and q_out must be 16-byte aligned";
+    if (!aligned(r->positions, 4) || !aligned(r->seqs, 4)) return "positions and seqs must be 4-byte aligned";
+    if (r->q && r->q == r->q_out && r->n_rows > 1 && r->q_stride != r->q_out_stride)
+        return "q_out in q's place needs q's stride";
+    if (!r->seqs && r->n_rows > c->n_seqs) return "more rows than sequences";
+    return nullptr;
+}
+
+static const char *attn_refusal(const moss_enc_kv_cache *c, const moss_enc_attn *p)
+{
+    if (p->n_q_heads < 1 || p->n_q_heads > 65535 || p->n_q_heads % c->n_kv_heads != 0 || p->max_len < 0)
+        return "n_q_heads must be a multiple of n_kv_heads, max_len not negative";
+    if (!row_type_ok(c, p->dtype)) return "q must be of the cache's 16-bit type (either with an e4m3 cache)";
+    if (!std::isfinite(p->scale)) return "scale must be finite";
+    const int64_t q_row = (int64_t)p->n_q_heads * c->head_dim;
+    if (p->q_stride % 8 != 0 || (c->n_seqs > 1 && p->q_stride < q_row))
+        return "q's rows overlap or are not multiples of 16 bytes apart";
+    if (c->n_seqs > 65535) return "more than 65535 sequences";
+    if (c->n_seqs == 0) return nullptr;
+    if (!p->q || !p->out || !p->lengths || !aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->lse, 4) ||
+        !aligned(p->lengths, 4))
+        return "q and out must be 16-byte aligned, lse and lengths 4-byte";
+    return nullptr;
+}
+
+extern "C" const char *moss_enc_paged_refusal(const moss_enc_kv_cache *cache, const moss_enc_kv_rows *rows,
+                                              const moss_enc_attn *attn)
+{
+    const char *why = cache_refusal(cache);
+    if (!why && rows) why = rows_refusal(cache, rows);
+    if (!why && attn) why = attn_refusal(cache, attn);
+    return why;
+}
+
+// The kernels' form of a checked cache.
+static PagedKV paged_kv(const moss_enc *h, const moss_enc_kv_cache *c)
+{
+    const int es = c->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2;
+    PagedKV o{};
+    o.k = static_cast<uint8_t *>(c->k);
+    o.v = static_cast<uint8_t *>(c->v);
+    o.table = c->page_table;
+    o.table_stride = c->table_stride;
+    o.stride_page = c->stride_page * es;
+    o.stride_token = c->stride_token * es;
+    o.stride_head = c->stride_head * es;
+    o.n_seqs = c->n_seqs;
+    o.pages_per_seq = c->pages_per_seq;
+    o.n_pages = c->n_pages;
+    o.page_shift = __builtin_ctz((unsigned)c->page_size);
+    o.hkv = c->n_kv_heads;
+    o.dim = c->head_dim;
+    o.k_scale = c->k_scale;
+    o.v_scale = c->v_scale;
+    o.flag = h->err + PAGE_FLAG_WORD;
+    return o;
+}
+
+extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, const moss_enc_kv_rows *r)
+{
+    if (!h) return MOSS_ENC_ERR_INVALID_ARG;
+    if (!r) return fail(h, MOSS_ENC_ERR_INVALID_ARG, "no rows");
+    if (const char *why = moss_enc_paged_refusal(cache, r, nullptr)) return fail(h, MOSS_ENC_ERR_INVALID_ARG, why);
+    if (r->n_rows == 0) return MOSS_ENC_OK;
+    const int64_t kv_row = (int64_t)cache->n_kv_heads * cache->head_dim, q_row = (int64_t)r->n_q_heads * cache->head_dim;
+    AppendArgs a{};
+    a.c = paged_kv(h, cache);
+    a.k = static_cast<const uint16_t *>(r->k);
+    a.v = static_cast<const uint16_t *>(r->v);
+    a.q = static_cast<const uint16_t *>(r->q);
+    a.q_out = static_cast<uint16_t *>(r->q_out);
+    a.k_stride = r->k_stride;
+    a.v_stride = r->v_stride;
+    a.q_stride = r->q_stride;
+    a.q_out_stride = r->q_out_stride;
+    a.positions = r->positions;
+    a.seqs = r->seqs;
+    a.inv_freq = r->inv_freq;
+    a.hq = r->n_q_heads;
+    a.rotary = r->rotary;
+    a.interleaved = r->interleaved;
+    const bool e4m3 = cache->dtype == MOSS_ENC_KV_E4M3;
+    a.inv_k_scale = e4m3 ? 1.0f / cache->k_scale : 1.0f;
+    a.inv_v_scale = e4m3 ? 1.0f / cache->v_scale : 1.0f;
+    OnDevice dev(h);
+    Launch L(h, "kv_append", 3.0 * r->n_rows * r->rotary * (r->n_q_heads + cache->n_kv_heads),
+             (double)r->n_rows * (4.0 * q_row + 2.0 * kv_row * (e4m3 ? 3 : 4) + 8.0));
+    const int items = (r->n_q_heads + 2 * cache->n_kv_heads) * (cache->head_dim / 16);
+    const dim3 grid(r->n_rows), block(std::min(256, std::max(64, (items + 31) / 32 * 32)));
+    if (r->dtype == MOSS_ENC_KV_BF16)
+        CUDA_TRY(h, launch_k(h, e4m3 ? kv_append_kernel<bf16, true> : kv_append_kernel<bf16, false>, grid, block, 0, a));
+    else
+        CUDA_TRY(h, launch_k(h, e4m3 ? kv_append_kernel<__half, true> : kv_append_kernel<__half, false>, grid, block, 0, a));
+    return MOSS_ENC_OK;
+}
+
+// Query heads of one key head that a CTA takes at once: one or two of the
+// matrix instruction's 8 columns (two cost twice the registers, which
+// head_dim 256 does not leave).
+static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
+
+extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_enc_kv_cache *cache, int n_q_heads, int max_len)
+{
+    if (!h || cache_refusal(cache) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || max_len < 0) return -1;
+    return 0;
+}
+
+template <typename T, typename QT, bool E4M3, int D, int NT>
+static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a)
+{
+    constexpr size_t smem = sizeof(float) * PagedState<T, E4M3, D, NT>::SLOT * (PA_WARPS / 2);
+    static_assert(smem <= 48 * 1024, "no attribute needed for the joined states");
+    CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, dim3(a.c.hkv * a.head_groups, a.c.n_seqs),
+                         dim3(32 * PA_WARPS), smem, a));
+    return MOSS_ENC_OK;
+}
+
+template <typename T, typename QT, bool E4M3>
+static moss_enc_status paged_attn_dim(moss_enc *h, const PagedAttnArgs &a, int columns)
+{
+    switch (a.c.dim) {
+    case 64: return columns == 2 ? paged_attn_run<T, QT, E4M3, 64, 2>(h, a) : paged_attn_run<T, QT, E4M3, 64, 1>(h, a);
+    case 128: return columns == 2 ? paged_attn_run<T, QT, E4M3, 128, 2>(h, a) : paged_attn_run<T, QT, E4M3, 128, 1>(h, a);
+    default: return paged_attn_run<T, QT, E4M3, 256, 1>(h, a);
+    }
+}
+
+extern "C" moss_enc_status moss_enc_paged_attn(moss_enc *h, const moss_enc_kv_cache *cache, const moss_enc_attn *p)
+{
+    if (!h) return MOSS_ENC_ERR_INVALID_ARG;
+    if (!p) return fail(h, MOSS_ENC_ERR_INVALID_ARG, "no queries");
+    if (const char *why = moss_enc_paged_refusal(cache, nullptr, p)) return fail(h, MOSS_ENC_ERR_INVALID_ARG, why);
+    if (cache->n_seqs == 0) return MOSS_ENC_OK;
+    const int64_t q_row = (int64_t)p->n_q_heads * cache->head_dim;
+    PagedAttnArgs a{};
+    a.c = paged_kv(h, cache);
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.out = static_cast<uint16_t *>(p->out);
+    a.lse = p->lse;
+    a.lengths = p->lengths;
+    a.q_stride = p->q_stride;
+    a.hq = p->n_q_heads;
+    a.group = p->n_q_heads / cache->n_kv_heads;
+    const int columns = attn_columns(cache, a.group);
+    a.head_groups = (a.group + 8 * columns - 1) / (8 * columns);
+    a.scale_log2 = p->scale * 1.4426950408889634f;
+    OnDevice dev(h);
+    // the lengths are on the device: profiles count the bound
+    const double tokens = (double)cache->n_seqs * (p->max_len > 0 ? p->max_len : (double)cache->pages_per_seq * cache->page_size);
+    Launch L(h, "paged_attn", 4.0 * tokens * q_row,
+             2.0 * tokens * cache->n_kv_heads * cache->head_dim * (cache->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2) +
+                 4.0 * cache->n_seqs * q_row);
+    if (cache->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<bf16, bf16, false>(h, a, columns);
+    if (cache->dtype == MOSS_ENC_KV_F16) return paged_attn_dim<__half, __half, false>(h, a, columns);
+    if (p->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<__half, bf16, true>(h, a, columns);
+    return paged_attn_dim<__half, __half, true>(h, a, columns);
 }
 
 // --------------------------------------------------------- GELU self-test

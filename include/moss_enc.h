@@ -21,8 +21,8 @@
  *    than the capacity fixed at create time returns MOSS_ENC_ERR_CAPACITY.
  *  - No C++ exception crosses this interface.  A handle is used by one host
  *    thread at a time.
- *  - Errors found on the device (a bounded wait that timed out) are reported
- *    by moss_enc_synchronize.
+ *  - Errors found on the device (a bounded wait that timed out, a page outside
+ *    a paged cache) are reported by moss_enc_synchronize.
  */
 #ifndef MOSS_ENC_H
 #define MOSS_ENC_H
@@ -195,7 +195,9 @@ moss_enc_status moss_enc_create(const moss_enc_config *cfg, const void *weights,
 moss_enc_status moss_enc_set_stream(moss_enc *h, void *stream);
 
 /* Wait for the handle's stream; return MOSS_ENC_ERR_DEVICE_TIMEOUT if a kernel
- * reported a timed-out wait since the last call (and clear the flag). */
+ * reported a timed-out wait since the last call, or MOSS_ENC_ERR_INVALID_ARG if
+ * one found a sequence, position, length or page outside a paged cache (and
+ * clear the flags). */
 moss_enc_status moss_enc_synchronize(moss_enc *h);
 
 /* Release a handle: synchronises its stream, then frees the weights, the
@@ -392,6 +394,143 @@ moss_enc_status moss_enc_nvf4_quant_rows(moss_enc *h, const float *x, void *code
  * (each row's part's g).  n/parts % 128 == 0, k % 64 == 0; INVALID_ARG
  * otherwise. */
 moss_enc_status moss_enc_nvf4_quant_weights(const void *w, int n, int k, int parts, void *codes, void *sfa, float *g);
+
+/* ------------------------------------------- one decoding step (few rows) */
+
+/* The adapter's rows replace the placeholder embeddings of a language model
+ * (page "MOSS-Transcribe-preview-2B - GGUF", "Architecture" table, "Audio
+ * injection"), which then runs one token at a time over a cache that grows
+ * with the audio (page "Ossicle-4B", "Long Audio": about 2.5 GB per hour).
+ * The calls below are the operators of one such step, each enqueued on the
+ * handle's stream, on memory that the caller owns; none of them reads the
+ * handle's weights, allocates, copies or waits, so all may be captured into
+ * CUDA graphs. */
+
+/* A few rows times a matrix of 4-bit codes with group scales (the form of
+ * moss_enc_gemm_q4's B, whose tiles start at 256 rows):
+ *   out[m][n] = epi(sum_g Bs[g][n] * sum_{k in g} x[m][k] * (code[n][k] - 8) + bias[n])
+ *  x          device bf16 (uint16 bits) [M][K], M 0..MOSS_ENC_GEMV_MAX_ROWS.
+ *  Bq, Bs     as moss_enc_gemm_q4: uint8 [N][K/2], fp32 [K/128][N].
+ *  bias       device fp32 [N], or NULL for none.
+ *  out, epilogue  as moss_enc_gemm: 0 (bf16), 1 (GELU, bf16), 2 (fp32, out +=),
+ *             5 (fp32).
+ * Any N >= 1; K % 128 == 0; x and Bq 16-byte aligned, Bs, bias and out aligned
+ * to their elements.  The sums are fp32 and the scale multiplies a group's
+ * sum, so no weight is rounded (moss_enc_gemm_q4 multiplies bf16(q * s)). */
+#define MOSS_ENC_GEMV_MAX_ROWS 32
+moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs, const float *bias,
+                                 void *out, int M, int N, int K, int epilogue);
+
+/* Element type of the cached keys and values. */
+enum { MOSS_ENC_KV_BF16 = 0, MOSS_ENC_KV_F16 = 1, MOSS_ENC_KV_E4M3 = 2 };
+
+/* A paged cache in the caller's memory: n_pages pages of page_size positions
+ * of n_kv_heads keys and values, and the pages of each sequence in order.
+ *  k, v       device, element (page, position, head, dim) at
+ *             page * stride_page + position * stride_token + head * stride_head
+ *             + dim (in elements, the same for k and v), so pages may hold
+ *             [position][head] or [head][position].
+ *  page_table device int32 [n_seqs][pages_per_seq], rows table_stride apart:
+ *             page i of a sequence holds its positions i * page_size ...
+ *             Entries past a sequence's last position are not read.
+ *  page_size  a power of two, 16 or more; n_pages >= 1; pages_per_seq >= 1 and
+ *             pages_per_seq * page_size < 2^31.
+ *  head_dim   64, 128 or 256.
+ *  dtype      MOSS_ENC_KV_*.  An e4m3 cache holds keys / k_scale and values /
+ *             v_scale (finite, > 0; not used by the 16-bit types), rounded to
+ *             nearest, ties to even, held at +-448.
+ * k, v and the strides are multiples of 16 bytes. */
+typedef struct {
+    void *k, *v;
+    const int32_t *page_table;
+    int64_t table_stride;
+    int64_t stride_page, stride_token, stride_head;
+    int n_seqs, pages_per_seq, n_pages, page_size;
+    int n_kv_heads, head_dim;
+    int dtype;
+    float k_scale, v_scale;
+} moss_enc_kv_cache;
+
+/* Rows to append: row r belongs to position positions[r] of sequence seqs[r].
+ *  k, v       device [n_rows][n_kv_heads][head_dim], rows k_stride / v_stride
+ *             elements apart (heads lie next to one another).
+ *  q, q_out   device [n_rows][n_q_heads][head_dim], rows q_stride / q_out_stride
+ *             apart: queries turned by the same angles; q_out may be q itself
+ *             (same stride).  Both NULL with n_q_heads 0.
+ *  dtype      of k, v, q and q_out: MOSS_ENC_KV_BF16 or MOSS_ENC_KV_F16, the
+ *             cache's own unless that is e4m3.
+ *  positions  device int32 [n_rows], >= 0.
+ *  seqs       device int32 [n_rows], or NULL when row r is sequence r's.  A row
+ *             with a negative sequence is padding: nothing of it is written.
+ *  inv_freq   device fp64 [rotary / 2]: dims of a pair i turn by the angle
+ *             positions[r] * inv_freq[i] (taken in 64 bits; the product in fp32).
+ *  rotary     leading dims of each key and query head that turn: a multiple of
+ *             16 up to head_dim, or 0 for none (inv_freq may then be NULL).
+ *  interleaved  0: pairs are (i, i + rotary/2); 1: (2i, 2i + 1).
+ * k, v, q, q_out and their strides are multiples of 16 bytes. */
+typedef struct {
+    const void *k, *v, *q;
+    void *q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    const int32_t *positions, *seqs;
+    const double *inv_freq;
+    int n_rows, n_q_heads, dtype, rotary, interleaved;
+} moss_enc_kv_rows;
+
+/* Turn the rows' keys (and queries) and write keys and values to the cache.
+ * Rows of one call must name different places (of two that name the same
+ * place either may be found there, in parts).  A row whose sequence, position
+ * or page is outside the cache is not written and is reported by the next
+ * moss_enc_synchronize (MOSS_ENC_ERR_INVALID_ARG). */
+moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, const moss_enc_kv_rows *rows);
+
+/* One new token per sequence of the cache:
+ *   out[s][h] = sum_{p < lengths[s]} softmax_p(scale * q[s][h] . k[s][p][h']) v[s][p][h'],
+ * h' = h / (n_q_heads / n_kv_heads), in fp32 (probabilities rounded to 16 bits
+ * for the product with the values, their sum not).
+ *  q          device [n_seqs][n_q_heads][head_dim], rows q_stride elements
+ *             apart; bf16 or f16 as dtype says, the cache's own type unless
+ *             that is e4m3.  16-byte aligned, q_stride a multiple of 8.
+ *  out        device [n_seqs][n_q_heads][head_dim] of dtype, 16-byte aligned.
+ *  lse        device fp32 [n_seqs][n_q_heads]: log sum_p exp(scale * q . k), or
+ *             NULL.
+ *  lengths    device int32 [n_seqs]: positions to attend, the new token's own
+ *             included.  0 gives zeros and -inf.
+ *  n_q_heads  a multiple of the cache's n_kv_heads.
+ *  max_len    a bound on the lengths that the caller knows (0: the table's
+ *             pages_per_seq * page_size); it sizes the launch and the
+ *             workspace, and longer sequences are still attended in full.
+ *  workspace  device, at least moss_enc_paged_attn_workspace() bytes, 16-byte
+ *             aligned (NULL when that is 0).  Nothing in it has to be set
+ *             before the call or kept after it, but calls whose work may
+ *             overlap (other streams, graphs replayed side by side) need one
+ *             each.
+ * A length or page outside the cache is clamped to it and reported by the next
+ * moss_enc_synchronize (MOSS_ENC_ERR_INVALID_ARG). */
+typedef struct {
+    const void *q;
+    void *out;
+    float *lse;
+    const int32_t *lengths;
+    int64_t q_stride;
+    int n_q_heads, dtype;
+    float scale;
+    int max_len;
+    void *workspace;
+    int64_t workspace_bytes;
+} moss_enc_attn;
+
+/* Why moss_enc_kv_append would refuse this cache and these rows, or
+ * moss_enc_paged_attn this cache and these queries (rows or attn may be NULL),
+ * or NULL if it would not.  Pure: no handle, no device. */
+const char *moss_enc_paged_refusal(const moss_enc_kv_cache *cache, const moss_enc_kv_rows *rows,
+                                   const moss_enc_attn *attn);
+
+/* Bytes of workspace that moss_enc_paged_attn needs for these heads and this
+ * bound on the lengths; -1 for arguments that it refuses. */
+int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_enc_kv_cache *cache, int n_q_heads, int max_len);
+
+moss_enc_status moss_enc_paged_attn(moss_enc *h, const moss_enc_kv_cache *cache, const moss_enc_attn *attn);
 
 /* The GEMM epilogues and conv1 evaluate GELU's erf with a short rational
  * approximation (Abramowitz & Stegun 7.1.28, error <= 3e-7), one value at a
