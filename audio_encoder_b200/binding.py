@@ -256,7 +256,7 @@ class KVCache:
                                 strides[2], page_table.shape[0], page_table.shape[1], n_pages, page, heads, dim,
                                 types[k.dtype], float(k_scale), float(v_scale))
         self.ref = ctypes.byref(self.desc)
-        self.workspaces = {}  # bytes by (query heads, bound on the lengths)
+        self.workspace = (None, 0)  # of the last (query heads, bound on the lengths) asked for: its bytes
 
 
 class Encoder:
@@ -515,13 +515,13 @@ class Encoder:
 
     def paged_attn_workspace(self, cache, heads: int, max_len: int = 0) -> int:
         """Bytes that paged_attn needs as workspace."""
-        key = (heads, int(max_len))
-        if key not in cache.workspaces:
+        key = (heads, max_len)
+        if cache.workspace[0] != key:
             need = int(lib().moss_enc_paged_attn_workspace(self.h, cache.ref, heads, int(max_len)))
             if need < 0:
                 raise MossEncError(1, "paged_attn: cache, heads or max_len refused")
-            cache.workspaces[key] = need
-        return cache.workspaces[key]
+            cache.workspace = (key, need)
+        return cache.workspace[1]
 
     def selftest_timeout(self, limit_ms: int = 50):
         self._check(lib().moss_enc_selftest_timeout(self.h, int(limit_ms)))

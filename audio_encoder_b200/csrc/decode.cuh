@@ -316,7 +316,7 @@ struct PagedState {
     static constexpr int VJ = VD / 2;                        // 16-dim tiles per piece
     static constexpr int TILES = D / 16;
     static constexpr int ESZ = E4M3 ? 1 : 2;
-    static constexpr int SLOT = NT * TILES * 4 * 32 + NT * 4 * 32;  // floats of a saved state
+    static constexpr int SLOT = NT * (TILES + 1) * 4 * 32;   // floats of a saved state
 
     uint32_t q[NT][TILES][2];
     float o[NT][TILES][4];
@@ -493,39 +493,44 @@ struct PagedState {
             }
     }
 
+    // A state in memory: 16 bytes a lane, o's tiles and then m and l.
     __device__ __forceinline__ void save(float *slot, int lane) const
     {
+        float4 *p = reinterpret_cast<float4 *>(slot) + lane;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
 #pragma unroll
             for (int i = 0; i < TILES; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) slot[((n * TILES + i) * 4 + j) * 32 + lane] = o[n][i][j];
-            float *st = slot + NT * TILES * 128 + n * 128 + lane;
-            st[0] = m[n][0], st[32] = m[n][1], st[64] = l[n][0], st[96] = l[n][1];
+                p[(n * (TILES + 1) + i) * 32] = make_float4(o[n][i][0], o[n][i][1], o[n][i][2], o[n][i][3]);
+            p[(n * (TILES + 1) + TILES) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
         }
     }
 
     // Joins a saved state of other positions: both sides to the larger maximum.
     __device__ __forceinline__ void join(const float *slot, int lane)
     {
+        const float4 *p = reinterpret_cast<const float4 *>(slot) + lane;
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            const float *st = slot + NT * TILES * 128 + n * 128 + lane;
+            const float4 st = p[(n * (TILES + 1) + TILES) * 32];
+            const float mb[2] = {st.x, st.y}, lb[2] = {st.z, st.w};
             float fa[2], fb[2];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float mb = st[32 * e], top = fmaxf(m[n][e], mb);
+                const float top = fmaxf(m[n][e], mb[e]);
                 fa[e] = top == -INFINITY ? 1.0f : ex2_approx(m[n][e] - top);
-                fb[e] = top == -INFINITY ? 1.0f : ex2_approx(mb - top);
+                fb[e] = top == -INFINITY ? 1.0f : ex2_approx(mb[e] - top);
                 m[n][e] = top;
-                l[n][e] = l[n][e] * fa[e] + st[64 + 32 * e] * fb[e];
+                l[n][e] = l[n][e] * fa[e] + lb[e] * fb[e];
             }
 #pragma unroll
-            for (int i = 0; i < TILES; i++)
-#pragma unroll
-                for (int j = 0; j < 4; j++)
-                    o[n][i][j] = o[n][i][j] * fa[j & 1] + slot[((n * TILES + i) * 4 + j) * 32 + lane] * fb[j & 1];
+            for (int i = 0; i < TILES; i++) {
+                const float4 v = p[(n * (TILES + 1) + i) * 32];
+                o[n][i][0] = o[n][i][0] * fa[0] + v.x * fb[0];
+                o[n][i][1] = o[n][i][1] * fa[1] + v.y * fb[1];
+                o[n][i][2] = o[n][i][2] * fa[0] + v.z * fb[0];
+                o[n][i][3] = o[n][i][3] * fa[1] + v.w * fb[1];
+            }
         }
     }
 
@@ -566,31 +571,154 @@ struct PagedState {
     }
 };
 
-// One CTA per (sequence, key head and its group of query heads).
+// The work of a launch is a row of tiles of PA_TILE positions, in the order
+// (sequence, key head and group of query heads, tile): the lengths are only
+// known on the device, so each CTA adds them up and takes an equal share of
+// the tiles. A share may end inside a unit (one sequence's key head); then the
+// unit's pieces go to the workspace and paged_join_kernel puts them together,
+// in the order of the positions, so results do not depend on timing.
+struct PagedSplit {
+    int s, unit, pieces;  // the unit that starts in this CTA's share and goes on in the next `pieces` shares
+};
+
+// Where a CTA's share starts.
+struct PagedShare {
+    long long first, count;  // tiles
+    long long share;         // tiles of a full share
+    int s;                   // first sequence
+    long long offset;        // tiles of that sequence before the share
+};
+
+__device__ __forceinline__ int paged_len(const PagedAttnArgs &a, int s, bool report)
+{
+    const int cap = a.c.pages_per_seq << a.c.page_shift, len = a.lengths[s];
+    if (len >= 0 && len <= cap) return len;
+    if (report) atomicOr(a.c.flag, DEV_ERR_PAGE);
+    return min(max(len, 0), cap);
+}
+
+// Thread i of the CTA adds up the tiles of its span of the sequences; a scan
+// over the spans gives the total and the span in which this CTA's share
+// starts, whose thread walks it.
+__device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int units)
+{
+    __shared__ long long warp_sums[PA_WARPS];
+    __shared__ long long found[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int span = (a.c.n_seqs + 32 * PA_WARPS - 1) / (32 * PA_WARPS);
+    const int lo = min(tid * span, a.c.n_seqs), hi = min(lo + span, a.c.n_seqs);
+    long long mine = 0;
+    for (int s = lo; s < hi; s++) mine += (long long)((paged_len(a, s, blockIdx.x == 0) + PA_TILE - 1) / PA_TILE) * units;
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
+    if (tid == 0) found[0] = a.c.n_seqs, found[1] = 0;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < PA_WARPS; w++) {
+        if (w < warp) before += warp_sums[w];
+        total += warp_sums[w];
+    }
+    PagedShare r;
+    r.share = max((total + gridDim.x - 1) / gridDim.x, 1ll);
+    r.first = min(r.share * blockIdx.x, total);
+    r.count = min(r.share, total - r.first);
+    long long at = before + upto - mine;
+    if (r.count > 0 && at <= r.first && r.first < at + mine) {
+        for (int s = lo; s < hi; s++) {
+            const long long t = (long long)((paged_len(a, s, false) + PA_TILE - 1) / PA_TILE) * units;
+            if (r.first < at + t) {
+                found[0] = s;
+                found[1] = r.first - at;
+                break;
+            }
+            at += t;
+        }
+    }
+    __syncthreads();
+    r.s = (int)found[0];
+    r.offset = found[1];
+    return r;
+}
+
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a)
+__global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a, float *pieces,
+                                                                                           PagedSplit *splits)
 {
     using S = PagedState<T, E4M3, D, NT>;
     extern __shared__ __align__(16) float pa_slots[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = blockIdx.x / a.head_groups, hg = blockIdx.x - head * a.head_groups, s = blockIdx.y;
+    const int units = a.c.hkv * a.head_groups;
     grid_dep_wait();
     grid_dep_launch();
-    const int cap = a.c.pages_per_seq << a.c.page_shift;
-    int len = a.lengths[s];
-    if (len < 0 || len > cap) {
-        if (tid == 0) atomicOr(a.c.flag, DEV_ERR_PAGE);
-        len = min(max(len, 0), cap);
+    PagedShare sh = paged_share(a, units);
+    PagedSplit split = {0, 0, 0};
+
+    // sequences without a position: nobody's share
+    for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x)
+        if (paged_len(a, s, false) == 0)
+            for (int i = tid; i < a.hq * (D / 8); i += 32 * PA_WARPS) {
+                *reinterpret_cast<uint4 *>(a.out + (long long)s * a.hq * D + 8 * i) = make_uint4(0, 0, 0, 0);
+                if (a.lse && i < a.hq) a.lse[(long long)s * a.hq + i] = -INFINITY;
+            }
+
+    S st;
+    for (int s = sh.s; sh.count > 0 && s < a.c.n_seqs; s++, sh.offset = 0) {
+        const int len = paged_len(a, s, false), tiles = (len + PA_TILE - 1) / PA_TILE;
+        if (tiles == 0) continue;
+        int unit = (int)(sh.offset / tiles), tile = (int)(sh.offset - (long long)unit * tiles);
+        for (; unit < units && sh.count > 0; unit++, tile = 0) {
+            const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
+            const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+            const int last = (int)min((long long)tiles, tile + sh.count);
+            st.clear();
+            st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f),
+                                   lane);
+            st.run(a.c, s, head, tile * PA_TILE, min(len, last * PA_TILE), warp, lane);
+            st.join_warps(pa_slots, warp, lane);
+            if (warp == 0) {
+                if (tile == 0 && last == tiles)
+                    st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D,
+                                          a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
+                                          E4M3 ? a.c.v_scale : 1.0f, lane);
+                else
+                    st.save(pieces + (2ll * blockIdx.x + (tile == 0)) * S::SLOT, lane);
+            }
+            if (tile == 0 && last < tiles) split = {s, unit, (int)((tiles - last + sh.share - 1) / sh.share)};
+            sh.count -= last - tile;
+        }
     }
-    const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    if (splits && tid == 0) splits[blockIdx.x] = split;
+}
+
+// CTA i joins the unit that was split from share i on: its first piece is the
+// share's second, the others are the first pieces of the next shares.
+template <typename T, typename QT, bool E4M3, int D, int NT>
+__global__ void __launch_bounds__(32 * PA_WARPS) paged_join_kernel(PagedAttnArgs a, const float *pieces, const PagedSplit *splits)
+{
+    using S = PagedState<T, E4M3, D, NT>;
+    extern __shared__ __align__(16) float pa_slots[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_dep_wait();
+    grid_dep_launch();
+    PagedSplit sp = splits[blockIdx.x];
+    if (sp.pieces == 0) return;
+    sp.pieces = min(sp.pieces, (int)(gridDim.x - 1 - blockIdx.x));
     S st;
     st.clear();
-    st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
-    st.run(a.c, s, head, 0, len, warp, lane);
+    for (int i = warp; i <= sp.pieces; i += PA_WARPS)
+        st.join(pieces + (2ll * (blockIdx.x + i) + (i == 0)) * S::SLOT, lane);
     st.join_warps(pa_slots, warp, lane);
-    if (warp == 0)
-        st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr,
-                              heads, E4M3 ? a.c.v_scale : 1.0f, lane);
+    if (warp != 0) return;
+    const int head = sp.unit / a.head_groups, hg = sp.unit - head * a.head_groups;
+    const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    st.template store<QT>(a.out + ((long long)sp.s * a.hq + h0) * D, a.lse ? a.lse + (long long)sp.s * a.hq + h0 : nullptr,
+                          heads, E4M3 ? a.c.v_scale : 1.0f, lane);
 }
 
 }  // namespace moss

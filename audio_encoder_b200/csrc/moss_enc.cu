@@ -2683,7 +2683,6 @@ static const char *attn_refusal(const moss_enc_kv_cache *c, const moss_enc_attn 
     const int64_t q_row = (int64_t)p->n_q_heads * c->head_dim;
     if (p->q_stride % 8 != 0 || (c->n_seqs > 1 && p->q_stride < q_row))
         return "q's rows overlap or are not multiples of 16 bytes apart";
-    if (c->n_seqs > 65535) return "more than 65535 sequences";
     if (c->n_seqs == 0) return nullptr;
     if (!p->q || !p->out || !p->lengths || !aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->lse, 4) ||
         !aligned(p->lengths, 4))
@@ -2767,29 +2766,75 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 // head_dim 256 does not leave).
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
+// The launch of paged_attn: CTAs, and whether a unit may be split between them.
+struct AttnGrid {
+    int ctas;
+    bool split;
+};
+
+static AttnGrid attn_grid(const moss_enc *h, const moss_enc_kv_cache *c, int group, int max_len)
+{
+    const int columns = attn_columns(c, group), head_groups = (group + 8 * columns - 1) / (8 * columns);
+    const int64_t cap = (int64_t)c->page_size * c->pages_per_seq;
+    const int64_t tiles = ((max_len > 0 ? std::min<int64_t>(max_len, cap) : cap) + PA_TILE - 1) / PA_TILE;
+    const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * head_groups;
+    const int resident = h->num_sms * (c->head_dim * columns <= 128 ? 2 : 1);
+    AttnGrid g;
+    g.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(units * tiles, resident));
+    // the bound may be wrong, so only what the cache itself holds rules a split out
+    g.split = cap > PA_TILE && g.ctas > 1;
+    return g;
+}
+
+// Bytes of one saved state: 8 columns' sums, maxima and outputs.
+static int64_t attn_slot_bytes(const moss_enc_kv_cache *c, int group)
+{
+    return (int64_t)attn_columns(c, group) * (c->head_dim / 16 + 1) * 128 * sizeof(float);
+}
+
+static int64_t attn_workspace(const moss_enc *h, const moss_enc_kv_cache *c, int group, int max_len)
+{
+    const AttnGrid g = attn_grid(h, c, group, max_len);
+    return g.split ? g.ctas * (2 * attn_slot_bytes(c, group) + (int64_t)sizeof(PagedSplit)) : 0;
+}
+
 extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_enc_kv_cache *cache, int n_q_heads, int max_len)
 {
     if (!h || cache_refusal(cache) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || max_len < 0) return -1;
-    return 0;
+    return attn_workspace(h, cache, n_q_heads / cache->n_kv_heads, max_len);
 }
 
 template <typename T, typename QT, bool E4M3, int D, int NT>
-static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a)
+static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const AttnGrid &g, void *workspace, double flops,
+                                      double bytes)
 {
-    constexpr size_t smem = sizeof(float) * PagedState<T, E4M3, D, NT>::SLOT * (PA_WARPS / 2);
+    using S = PagedState<T, E4M3, D, NT>;
+    constexpr size_t smem = sizeof(float) * S::SLOT * (PA_WARPS / 2);
     static_assert(smem <= 48 * 1024, "no attribute needed for the joined states");
-    CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, dim3(a.c.hkv * a.head_groups, a.c.n_seqs),
-                         dim3(32 * PA_WARPS), smem, a));
+    float *pieces = static_cast<float *>(workspace);
+    PagedSplit *splits = g.split ? reinterpret_cast<PagedSplit *>(pieces + (size_t)g.ctas * 2 * S::SLOT) : nullptr;
+    {
+        Launch L(h, "paged_attn", flops, bytes);
+        CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, dim3(g.ctas), dim3(32 * PA_WARPS), smem, a, pieces, splits));
+    }
+    if (g.split) {
+        Launch L(h, "paged_join", 0, 0);
+        CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, dim3(g.ctas), dim3(32 * PA_WARPS), smem, a,
+                             (const float *)pieces, (const PagedSplit *)splits));
+    }
     return MOSS_ENC_OK;
 }
 
 template <typename T, typename QT, bool E4M3>
-static moss_enc_status paged_attn_dim(moss_enc *h, const PagedAttnArgs &a, int columns)
+static moss_enc_status paged_attn_dim(moss_enc *h, const PagedAttnArgs &a, int columns, const AttnGrid &g, void *ws, double flops,
+                                      double bytes)
 {
-    switch (a.c.dim) {
-    case 64: return columns == 2 ? paged_attn_run<T, QT, E4M3, 64, 2>(h, a) : paged_attn_run<T, QT, E4M3, 64, 1>(h, a);
-    case 128: return columns == 2 ? paged_attn_run<T, QT, E4M3, 128, 2>(h, a) : paged_attn_run<T, QT, E4M3, 128, 1>(h, a);
-    default: return paged_attn_run<T, QT, E4M3, 256, 1>(h, a);
+    switch (a.c.dim + columns) {
+    case 65: return paged_attn_run<T, QT, E4M3, 64, 1>(h, a, g, ws, flops, bytes);
+    case 66: return paged_attn_run<T, QT, E4M3, 64, 2>(h, a, g, ws, flops, bytes);
+    case 129: return paged_attn_run<T, QT, E4M3, 128, 1>(h, a, g, ws, flops, bytes);
+    case 130: return paged_attn_run<T, QT, E4M3, 128, 2>(h, a, g, ws, flops, bytes);
+    default: return paged_attn_run<T, QT, E4M3, 256, 1>(h, a, g, ws, flops, bytes);
     }
 }
 
@@ -2812,16 +2857,21 @@ extern "C" moss_enc_status moss_enc_paged_attn(moss_enc *h, const moss_enc_kv_ca
     const int columns = attn_columns(cache, a.group);
     a.head_groups = (a.group + 8 * columns - 1) / (8 * columns);
     a.scale_log2 = p->scale * 1.4426950408889634f;
-    OnDevice dev(h);
+    const AttnGrid g = attn_grid(h, cache, a.group, p->max_len);
+    const int64_t need = attn_workspace(h, cache, a.group, p->max_len);
+    if (need > 0 && (!p->workspace || !aligned(p->workspace, 16) || p->workspace_bytes < need))
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "workspace missing, misaligned or too small");
     // the lengths are on the device: profiles count the bound
     const double tokens = (double)cache->n_seqs * (p->max_len > 0 ? p->max_len : (double)cache->pages_per_seq * cache->page_size);
-    Launch L(h, "paged_attn", 4.0 * tokens * q_row,
-             2.0 * tokens * cache->n_kv_heads * cache->head_dim * (cache->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2) +
-                 4.0 * cache->n_seqs * q_row);
-    if (cache->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<bf16, bf16, false>(h, a, columns);
-    if (cache->dtype == MOSS_ENC_KV_F16) return paged_attn_dim<__half, __half, false>(h, a, columns);
-    if (p->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<__half, bf16, true>(h, a, columns);
-    return paged_attn_dim<__half, __half, true>(h, a, columns);
+    const double flops = 4.0 * tokens * q_row;
+    const double bytes = 2.0 * tokens * cache->n_kv_heads * cache->head_dim * (cache->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2) +
+                         4.0 * cache->n_seqs * q_row;
+    OnDevice dev(h);
+    void *ws = p->workspace;
+    if (cache->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<bf16, bf16, false>(h, a, columns, g, ws, flops, bytes);
+    if (cache->dtype == MOSS_ENC_KV_F16) return paged_attn_dim<__half, __half, false>(h, a, columns, g, ws, flops, bytes);
+    if (p->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<__half, bf16, true>(h, a, columns, g, ws, flops, bytes);
+    return paged_attn_dim<__half, __half, true>(h, a, columns, g, ws, flops, bytes);
 }
 
 // --------------------------------------------------------- GELU self-test

@@ -571,6 +571,22 @@ def test_paged_attn_bound_on_the_lengths(enc):
         check_attn(enc, cache, q, lengths, max_len=bound)
 
 
+def test_paged_attn_refuses_a_workspace_that_is_too_small(enc):
+    g = gen(64)
+    cache = make_cache(2, 3000, 16, 2, 64, BF16, g)
+    q = randn((2, 4, 64), g, BF16)
+    n = torch.tensor([3000, 6], dtype=torch.int32, device="cuda")
+    need = enc.paged_attn_workspace(cache, 4)
+    assert need > 0
+    big = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
+    for bad in (big[:need - 1], big[8:8 + need], big[::2], big.view(torch.int8)):
+        with pytest.raises((ValueError, binding.MossEncError)):
+            enc.paged_attn(cache, q, n, workspace=bad)
+    check_attn(enc, cache, q, [3000, 6], workspace=big)
+    short = make_cache(2, 100, 16, 2, 64, BF16, g)
+    assert enc.paged_attn_workspace(short, 4) == 0
+
+
 def test_paged_attn_reports_lengths_and_pages_outside_the_cache(enc):
     g = gen(40)
     cache = make_cache(2, 64, 16, 1, 64, BF16, g)
