@@ -266,30 +266,43 @@ __device__ __forceinline__ uint2 ldg_stream8(const void *p)
     return v;
 }
 
-// W words of 16-bit pairs of consecutive dims, from a 16-bit or an e4m3 cache.
-template <bool E4M3, int W>
-__device__ __forceinline__ void load_dims(const uint8_t *p, uint32_t (&w)[W])
-{
-    if constexpr (!E4M3) {
-        static_assert(W == 4, "16 bytes");
-        const uint4 v = ldg_stream16(p);
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (W == 4) {
-        const uint2 v = ldg_stream8(p);
-        w[0] = e4m3x2_to_half2(v.x), w[1] = e4m3x2_to_half2(v.x >> 16);
-        w[2] = e4m3x2_to_half2(v.y), w[3] = e4m3x2_to_half2(v.y >> 16);
-    } else {
-        static_assert(W == 8, "16 bytes");
-        const uint4 v = ldg_stream16(p);
-        w[0] = e4m3x2_to_half2(v.x), w[1] = e4m3x2_to_half2(v.x >> 16);
-        w[2] = e4m3x2_to_half2(v.y), w[3] = e4m3x2_to_half2(v.y >> 16);
-        w[4] = e4m3x2_to_half2(v.z), w[5] = e4m3x2_to_half2(v.z >> 16);
-        w[6] = e4m3x2_to_half2(v.w), w[7] = e4m3x2_to_half2(v.w >> 16);
+// Consecutive dims of one row as they lie in the cache: 16 bytes, or the 8
+// that 8 dims of an e4m3 row take.
+template <int BYTES>
+struct RawDims {
+    uint32_t w[BYTES / 4];
+    __device__ __forceinline__ void load(const uint8_t *p)
+    {
+        if constexpr (BYTES == 16) {
+            const uint4 v = ldg_stream16(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        } else {
+            const uint2 v = ldg_stream8(p);
+            w[0] = v.x, w[1] = v.y;
+        }
     }
-}
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < BYTES / 4; i++) w[i] = 0;
+    }
+    // Dims 2 i and 2 i + 1 as a 16-bit pair.
+    template <bool E4M3>
+    __device__ __forceinline__ uint32_t pair(int i) const
+    {
+        return E4M3 ? e4m3x2_to_half2(w[i >> 1] >> (16 * (i & 1))) : w[i];
+    }
+};
 
 static constexpr int PA_WARPS = 8;
-static constexpr int PA_TILE = 16 * PA_WARPS;  // positions that a CTA's warps take at once
+
+// Positions that a warp takes in one step, in sixteens: as many as keep 8 KB
+// of the cache on its way per warp (128 KB an SM with 16 warps; an e4m3 cache
+// read 16 positions at a time had half of that and reached 53 % of the copy
+// rate).
+__host__ __device__ constexpr int pa_sub(int dim, bool e4m3) { return dim >= 256 ? 1 : (dim == 128 ? 1 : 2) * (e4m3 ? 2 : 1); }
+// Positions that the CTA's warps take at once.
+__host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_WARPS * pa_sub(dim, e4m3); }
 
 // What a warp holds of up to 8 NT query heads that share a key head, over the
 // positions it has seen: with s = scale log2(e) q.k, the running maximum m,
@@ -316,6 +329,7 @@ struct PagedState {
     static constexpr int VJ = VD / 2;                        // 16-dim tiles per piece
     static constexpr int TILES = D / 16;
     static constexpr int ESZ = E4M3 ? 1 : 2;
+    static constexpr int SUB = pa_sub(D, E4M3), TILE = pa_tile(D, E4M3);
     static constexpr int SLOT = NT * (TILES + 1) * 4 * 32;   // floats of a saved state
 
     uint32_t q[NT][TILES][2];
@@ -391,43 +405,65 @@ struct PagedState {
         }
     }
 
-    // Positions p0 .. p0 + 15 (one page; those at or past `end` are masked),
-    // whose keys and values start at kp and vp, rows `stride` bytes apart.
-    __device__ __forceinline__ void step(const uint8_t *kp, const uint8_t *vp, long long stride, int p0, int end, int lane)
+    // Positions p0 .. p0 + 16 SUB - 1, those at or past `end` masked. off[i]:
+    // where position p0 + 16 i lies (sixteen positions share a page), or one
+    // before it when that is past the end.
+    __device__ __forceinline__ void step(const PagedKV &c, const long long (&off)[SUB], int p0, int end, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
-        const uint8_t *k0 = kp + g * stride + t * 16, *k1 = k0 + 8 * stride;
-        const uint8_t *v0 = vp + 2 * t * stride + g * VD * ESZ;
-        uint32_t ka[KJ][KD / 2], kb[KJ][KD / 2];
+        RawDims<16> k[SUB][2][KJ];
+        RawDims<VD * ESZ> v[SUB][VI][4];
 #pragma unroll
-        for (int j = 0; j < KJ; j++) {
-            load_dims<E4M3>(k0 + 64 * j, ka[j]);
-            load_dims<E4M3>(k1 + 64 * j, kb[j]);
+        for (int u = 0; u < SUB; u++) {
+            const uint8_t *p = c.k + off[u] + g * c.stride_token + t * 16;
+#pragma unroll
+            for (int j = 0; j < KJ; j++) {
+                k[u][0][j].load(p + 64 * j);
+                k[u][1][j].load(p + 8 * c.stride_token + 64 * j);
+            }
         }
-        uint32_t v[VI][4][VJ];
 #pragma unroll
-        for (int i = 0; i < VI; i++) {
-            load_dims<E4M3>(v0 + i * 8 * VD * ESZ, v[i][0]);
-            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + stride, v[i][1]);
-            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + 8 * stride, v[i][2]);
-            load_dims<E4M3>(v0 + i * 8 * VD * ESZ + 9 * stride, v[i][3]);
+        for (int u = 0; u < SUB; u++) {
+            const uint8_t *p = c.v + off[u] + 2 * t * c.stride_token + g * VD * ESZ;
+#pragma unroll
+            for (int i = 0; i < VI; i++) {
+                v[u][i][0].load(p + i * 8 * VD * ESZ);
+                v[u][i][1].load(p + i * 8 * VD * ESZ + c.stride_token);
+                v[u][i][2].load(p + i * 8 * VD * ESZ + 8 * c.stride_token);
+                v[u][i][3].load(p + i * 8 * VD * ESZ + 9 * c.stride_token);
+            }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[SUB][NT][2];
+        float s[SUB][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; n++) {
-            float s[4] = {};
+        for (int u = 0; u < SUB; u++) {
+#pragma unroll
+            for (int n = 0; n < NT; n++) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KJ; j++)
 #pragma unroll
-                for (int e = 0; e < KD / 4; e++)
-                    mma_16816(T(), s, ka[j][2 * e], kb[j][2 * e], ka[j][2 * e + 1], kb[j][2 * e + 1],
-                              q[n][j * (KD / 4) + e][0], q[n][j * (KD / 4) + e][1]);
-            // s: positions g (0, 1) and g + 8 (2, 3), heads 2t and 2t + 1
-            s[0] = p0 + g < end ? s[0] * sc[n][0] : -INFINITY;
-            s[1] = p0 + g < end ? s[1] * sc[n][1] : -INFINITY;
-            s[2] = p0 + g + 8 < end ? s[2] * sc[n][0] : -INFINITY;
-            s[3] = p0 + g + 8 < end ? s[3] * sc[n][1] : -INFINITY;
-            float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
+                for (int e = 0; e < KD / 4; e++) {
+                    const uint32_t a0 = k[u][0][j].template pair<E4M3>(2 * e), a1 = k[u][1][j].template pair<E4M3>(2 * e);
+                    const uint32_t a2 = k[u][0][j].template pair<E4M3>(2 * e + 1), a3 = k[u][1][j].template pair<E4M3>(2 * e + 1);
+#pragma unroll
+                    for (int n = 0; n < NT; n++)
+                        mma_16816(T(), s[u][n], a0, a1, a2, a3, q[n][j * (KD / 4) + e][0], q[n][j * (KD / 4) + e][1]);
+                }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            // positions g (0, 1) and g + 8 (2, 3) of each sixteen, heads 2t and 2t + 1
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < SUB; u++) {
+                const bool lo = p0 + 16 * u + g < end, hi = p0 + 16 * u + g + 8 < end;
+                s[u][n][0] = lo ? s[u][n][0] * sc[n][0] : -INFINITY;
+                s[u][n][1] = lo ? s[u][n][1] * sc[n][1] : -INFINITY;
+                s[u][n][2] = hi ? s[u][n][2] * sc[n][0] : -INFINITY;
+                s[u][n][3] = hi ? s[u][n][3] * sc[n][1] : -INFINITY;
+                t0 = fmaxf(t0, fmaxf(s[u][n][0], s[u][n][2]));
+                t1 = fmaxf(t1, fmaxf(s[u][n][1], s[u][n][3]));
+            }
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, x));
@@ -445,44 +481,55 @@ struct PagedState {
                 }
             }
             const float b0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], b1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-            s[0] = ex2_approx(s[0] - b0), s[1] = ex2_approx(s[1] - b1);
-            s[2] = ex2_approx(s[2] - b0), s[3] = ex2_approx(s[3] - b1);
-            l[n][0] += s[0] + s[2], l[n][1] += s[1] + s[3];
-            // the probabilities are rounded to the cache's 16-bit type for
-            // the product (half an ulp each, errors that average out over the
-            // positions); their sum keeps 32 bits
-            pb[n][0] = movmatrix(from_f2<T>(s[0], s[1]));
-            pb[n][1] = movmatrix(from_f2<T>(s[2], s[3]));
+#pragma unroll
+            for (int u = 0; u < SUB; u++) {
+                const float e0 = ex2_approx(s[u][n][0] - b0), e1 = ex2_approx(s[u][n][1] - b1);
+                const float e2 = ex2_approx(s[u][n][2] - b0), e3 = ex2_approx(s[u][n][3] - b1);
+                l[n][0] += e0 + e2, l[n][1] += e1 + e3;
+                // the probabilities are rounded to the cache's 16-bit type
+                // for the product (half an ulp each, errors that average out
+                // over the positions); their sum keeps 32 bits
+                pb[u][n][0] = movmatrix(from_f2<T>(e0, e1));
+                pb[u][n][1] = movmatrix(from_f2<T>(e2, e3));
+            }
         }
-        if (p0 + 16 > end) {
+        if (p0 + 16 * SUB > end) {
             // masked rows hold anything: 0 * NaN must not reach the sum
 #pragma unroll
-            for (int r = 0; r < 4; r++)
-                if (p0 + 2 * t + (r & 1) + 4 * (r & 2) >= end)
+            for (int u = 0; u < SUB; u++)
 #pragma unroll
-                    for (int i = 0; i < VI; i++)
+                for (int r = 0; r < 4; r++)
+                    if (p0 + 16 * u + 2 * t + (r & 1) + 4 * (r & 2) >= end)
 #pragma unroll
-                        for (int j = 0; j < VJ; j++) v[i][r][j] = 0;
+                        for (int i = 0; i < VI; i++) v[u][i][r].zero();
         }
 #pragma unroll
-        for (int i = 0; i < VI; i++)
+        for (int u = 0; u < SUB; u++)
 #pragma unroll
-            for (int j = 0; j < VJ; j++) {
-                const uint32_t a0 = __byte_perm(v[i][0][j], v[i][1][j], 0x5410), a1 = __byte_perm(v[i][0][j], v[i][1][j], 0x7632);
-                const uint32_t a2 = __byte_perm(v[i][2][j], v[i][3][j], 0x5410), a3 = __byte_perm(v[i][2][j], v[i][3][j], 0x7632);
+            for (int i = 0; i < VI; i++)
 #pragma unroll
-                for (int n = 0; n < NT; n++) mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-            }
+                for (int j = 0; j < VJ; j++) {
+                    const uint32_t w0 = v[u][i][0].template pair<E4M3>(j), w1 = v[u][i][1].template pair<E4M3>(j);
+                    const uint32_t w2 = v[u][i][2].template pair<E4M3>(j), w3 = v[u][i][3].template pair<E4M3>(j);
+                    const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
+                    const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+#pragma unroll
+                    for (int n = 0; n < NT; n++) mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[u][n][0], pb[u][n][1]);
+                }
     }
 
-    // Positions [t0, end) of one key head of sequence s, 16 at a time, by the
-    // CTA's warps in turn.
+    // Positions [t0, end) of one key head of sequence s, by the CTA's warps in
+    // turn.
     __device__ __forceinline__ void run(const PagedKV &c, int s, int head, int t0, int end, int warp, int lane)
     {
-        for (int p0 = t0 + 16 * warp; p0 < end; p0 += PA_TILE) {
-            const int page = max(c.page_of(s, p0), 0);
-            const long long off = c.at(page, p0) + head * c.stride_head;
-            step(c.k + off, c.v + off, c.stride_token, p0, end, lane);
+        for (int p0 = t0 + 16 * SUB * warp; p0 < end; p0 += TILE) {
+            long long off[SUB];
+#pragma unroll
+            for (int u = 0; u < SUB; u++) {
+                const int p = min(p0 + 16 * u, (end - 1) & ~15);
+                off[u] = c.at(max(c.page_of(s, p), 0), p) + head * c.stride_head;
+            }
+            step(c, off, p0, end, lane);
         }
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -571,7 +618,7 @@ struct PagedState {
     }
 };
 
-// The work of a launch is a row of tiles of PA_TILE positions, in the order
+// The work of a launch is a row of tiles, in the order
 // (sequence, key head and group of query heads, tile): the lengths are only
 // known on the device, so each CTA adds them up and takes an equal share of
 // the tiles. A share may end inside a unit (one sequence's key head); then the
@@ -600,6 +647,7 @@ __device__ __forceinline__ int paged_len(const PagedAttnArgs &a, int s, bool rep
 // Thread i of the CTA adds up the tiles of its span of the sequences; a scan
 // over the spans gives the total and the span in which this CTA's share
 // starts, whose thread walks it.
+template <int TILE>
 __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int units)
 {
     __shared__ long long warp_sums[PA_WARPS];
@@ -608,7 +656,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
     const int span = (a.c.n_seqs + 32 * PA_WARPS - 1) / (32 * PA_WARPS);
     const int lo = min(tid * span, a.c.n_seqs), hi = min(lo + span, a.c.n_seqs);
     long long mine = 0;
-    for (int s = lo; s < hi; s++) mine += (long long)((paged_len(a, s, blockIdx.x == 0) + PA_TILE - 1) / PA_TILE) * units;
+    for (int s = lo; s < hi; s++) mine += (long long)((paged_len(a, s, blockIdx.x == 0) + TILE - 1) / TILE) * units;
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -631,7 +679,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
     long long at = before + upto - mine;
     if (r.count > 0 && at <= r.first && r.first < at + mine) {
         for (int s = lo; s < hi; s++) {
-            const long long t = (long long)((paged_len(a, s, false) + PA_TILE - 1) / PA_TILE) * units;
+            const long long t = (long long)((paged_len(a, s, false) + TILE - 1) / TILE) * units;
             if (r.first < at + t) {
                 found[0] = s;
                 found[1] = r.first - at;
@@ -647,7 +695,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
 }
 
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a, float *pieces,
+__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a, float *pieces,
                                                                                            PagedSplit *splits)
 {
     using S = PagedState<T, E4M3, D, NT>;
@@ -656,7 +704,7 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_at
     const int units = a.c.hkv * a.head_groups;
     grid_dep_wait();
     grid_dep_launch();
-    PagedShare sh = paged_share(a, units);
+    PagedShare sh = paged_share<S::TILE>(a, units);
     PagedSplit split = {0, 0, 0};
 
     // sequences without a position: nobody's share
@@ -669,7 +717,7 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_at
 
     S st;
     for (int s = sh.s; sh.count > 0 && s < a.c.n_seqs; s++, sh.offset = 0) {
-        const int len = paged_len(a, s, false), tiles = (len + PA_TILE - 1) / PA_TILE;
+        const int len = paged_len(a, s, false), tiles = (len + S::TILE - 1) / S::TILE;
         if (tiles == 0) continue;
         int unit = (int)(sh.offset / tiles), tile = (int)(sh.offset - (long long)unit * tiles);
         for (; unit < units && sh.count > 0; unit++, tile = 0) {
@@ -679,7 +727,7 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_at
             st.clear();
             st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f),
                                    lane);
-            st.run(a.c, s, head, tile * PA_TILE, min(len, last * PA_TILE), warp, lane);
+            st.run(a.c, s, head, tile * S::TILE, min(len, last * S::TILE), warp, lane);
             st.join_warps(pa_slots, warp, lane);
             if (warp == 0) {
                 if (tile == 0 && last == tiles)
@@ -693,7 +741,31 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D * NT <= 128 ? 2 : 1) paged_at
             sh.count -= last - tile;
         }
     }
-    if (splits && tid == 0) splits[blockIdx.x] = split;
+    if (tid == 0) splits[blockIdx.x] = split;
+}
+
+// One CTA per unit, for lengths that are not worth splitting.
+template <typename T, typename QT, bool E4M3, int D, int NT>
+__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_units_kernel(PagedAttnArgs a)
+{
+    using S = PagedState<T, E4M3, D, NT>;
+    extern __shared__ __align__(16) float pa_slots[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int units = a.c.hkv * a.head_groups;
+    const int s = blockIdx.x / units, unit = blockIdx.x - s * units;
+    const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
+    const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    grid_dep_wait();
+    grid_dep_launch();
+    const int len = paged_len(a, s, threadIdx.x == 0);
+    S st;
+    st.clear();
+    st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
+    st.run(a.c, s, head, 0, len, warp, lane);
+    st.join_warps(pa_slots, warp, lane);
+    if (warp == 0)
+        st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr,
+                              heads, E4M3 ? a.c.v_scale : 1.0f, lane);
 }
 
 // CTA i joins the unit that was split from share i on: its first piece is the

@@ -2676,6 +2676,7 @@ static const char *rows_refusal(const moss_enc_kv_cache *c, const moss_enc_kv_ro
 
 static const char *attn_refusal(const moss_enc_kv_cache *c, const moss_enc_attn *p)
 {
+    if ((int64_t)c->n_seqs * c->n_kv_heads * ((p->n_q_heads / c->n_kv_heads + 7) / 8) > INT32_MAX) return "too many sequences and heads";
     if (p->n_q_heads < 1 || p->n_q_heads > 65535 || p->n_q_heads % c->n_kv_heads != 0 || p->max_len < 0)
         return "n_q_heads must be a multiple of n_kv_heads, max_len not negative";
     if (!row_type_ok(c, p->dtype)) return "q must be of the cache's 16-bit type (either with an e4m3 cache)";
@@ -2766,9 +2767,13 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 // head_dim 256 does not leave).
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
-// The launch of paged_attn: CTAs, and whether a unit may be split between them.
+// The launch of paged_attn: one CTA per unit (a sequence's key head), or
+// shares of tiles that may split units and a join after it.  Up to
+// ATTN_WHOLE positions a unit is left whole.
+constexpr int ATTN_WHOLE = 512;
+
 struct AttnGrid {
-    int ctas;
+    int64_t ctas;
     bool split;
 };
 
@@ -2776,14 +2781,12 @@ static AttnGrid attn_grid(const moss_enc *h, const moss_enc_kv_cache *c, int gro
 {
     const int columns = attn_columns(c, group), head_groups = (group + 8 * columns - 1) / (8 * columns);
     const int64_t cap = (int64_t)c->page_size * c->pages_per_seq;
-    const int64_t tiles = ((max_len > 0 ? std::min<int64_t>(max_len, cap) : cap) + PA_TILE - 1) / PA_TILE;
+    const int64_t bound = max_len > 0 ? std::min<int64_t>(max_len, cap) : cap;
+    const int tile = pa_tile(c->head_dim, c->dtype == MOSS_ENC_KV_E4M3);
     const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * head_groups;
-    const int resident = h->num_sms * (c->head_dim * columns <= 128 ? 2 : 1);
-    AttnGrid g;
-    g.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(units * tiles, resident));
-    // the bound may be wrong, so only what the cache itself holds rules a split out
-    g.split = cap > PA_TILE && g.ctas > 1;
-    return g;
+    if (bound <= ATTN_WHOLE) return AttnGrid{units, false};
+    const int resident = h->num_sms * (c->head_dim <= 128 && columns == 1 ? 2 : 1);
+    return AttnGrid{std::max<int64_t>(1, std::min<int64_t>(units * ((bound + tile - 1) / tile), resident)), true};
 }
 
 // Bytes of one saved state: 8 columns' sums, maxima and outputs.
@@ -2811,17 +2814,21 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
     using S = PagedState<T, E4M3, D, NT>;
     constexpr size_t smem = sizeof(float) * S::SLOT * (PA_WARPS / 2);
     static_assert(smem <= 48 * 1024, "no attribute needed for the joined states");
+    const dim3 grid((unsigned)g.ctas), block(32 * PA_WARPS);
+    if (!g.split) {
+        Launch L(h, "paged_attn", flops, bytes);
+        CUDA_TRY(h, launch_k(h, paged_attn_units_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a));
+        return MOSS_ENC_OK;
+    }
     float *pieces = static_cast<float *>(workspace);
-    PagedSplit *splits = g.split ? reinterpret_cast<PagedSplit *>(pieces + (size_t)g.ctas * 2 * S::SLOT) : nullptr;
+    PagedSplit *splits = reinterpret_cast<PagedSplit *>(pieces + (size_t)g.ctas * 2 * S::SLOT);
     {
         Launch L(h, "paged_attn", flops, bytes);
-        CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, dim3(g.ctas), dim3(32 * PA_WARPS), smem, a, pieces, splits));
+        CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, pieces, splits));
     }
-    if (g.split) {
-        Launch L(h, "paged_join", 0, 0);
-        CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, dim3(g.ctas), dim3(32 * PA_WARPS), smem, a,
-                             (const float *)pieces, (const PagedSplit *)splits));
-    }
+    Launch L(h, "paged_join", 0, 0);
+    CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, (const float *)pieces,
+                         (const PagedSplit *)splits));
     return MOSS_ENC_OK;
 }
 

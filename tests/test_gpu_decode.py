@@ -584,7 +584,7 @@ def test_paged_attn_refuses_a_workspace_that_is_too_small(enc):
             enc.paged_attn(cache, q, n, workspace=bad)
     check_attn(enc, cache, q, [3000, 6], workspace=big)
     short = make_cache(2, 100, 16, 2, 64, BF16, g)
-    assert enc.paged_attn_workspace(short, 4) == 0
+    assert enc.paged_attn_workspace(short, 4) == 0 and enc.paged_attn_workspace(cache, 4, max_len=100) == 0
 
 
 def test_paged_attn_reports_lengths_and_pages_outside_the_cache(enc):
