@@ -253,10 +253,18 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t v)
     return r;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v)
+// The lower and the upper two of four e4m3 values as f16 pairs (exact).
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t v)
 {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v & 0xFFFFu), __NV_E4M3);
-    return (uint32_t)r.x | ((uint32_t)r.y << 16);
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t v)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
+    return r;
 }
 
 __device__ __forceinline__ uint2 ldg_stream8(const void *p)
@@ -290,9 +298,24 @@ struct RawDims {
     template <bool E4M3>
     __device__ __forceinline__ uint32_t pair(int i) const
     {
-        return E4M3 ? e4m3x2_to_half2(w[i >> 1] >> (16 * (i & 1))) : w[i];
+        return !E4M3 ? w[i] : i & 1 ? e4m3_hi(w[i >> 1]) : e4m3_lo(w[i >> 1]);
     }
 };
+
+// Dims 2 i and 2 i + 1 of two rows, turned: {row a, row b} of each dim as a
+// pair. For e4m3 the bytes are paired first, which takes half the shuffles.
+template <bool E4M3, int BYTES>
+__device__ __forceinline__ void row_pairs(const RawDims<BYTES> &a, const RawDims<BYTES> &b, int i, uint32_t &even, uint32_t &odd)
+{
+    if constexpr (E4M3) {
+        const uint32_t v = __byte_perm(a.w[i >> 1], b.w[i >> 1], i & 1 ? 0x7362 : 0x5140);
+        even = e4m3_lo(v);
+        odd = e4m3_hi(v);
+    } else {
+        even = __byte_perm(a.w[i], b.w[i], 0x5410);
+        odd = __byte_perm(a.w[i], b.w[i], 0x7632);
+    }
+}
 
 static constexpr int PA_WARPS = 8;
 
@@ -327,7 +350,7 @@ struct PagedState {
     static constexpr int VD = E4M3 && D >= 128 ? 16 : 8;     // dims in a lane's piece of a value row
     static constexpr int VI = D / (8 * VD);                  // pieces
     static constexpr int VJ = VD / 2;                        // 16-dim tiles per piece
-    static constexpr int TILES = D / 16;
+    static constexpr int TILES = D / 16, DIM = D, COLUMNS = NT;
     static constexpr int ESZ = E4M3 ? 1 : 2;
     static constexpr int SUB = pa_sub(D, E4M3), TILE = pa_tile(D, E4M3);
     static constexpr int SLOT = NT * (TILES + 1) * 4 * 32;   // floats of a saved state
@@ -509,10 +532,9 @@ struct PagedState {
             for (int i = 0; i < VI; i++)
 #pragma unroll
                 for (int j = 0; j < VJ; j++) {
-                    const uint32_t w0 = v[u][i][0].template pair<E4M3>(j), w1 = v[u][i][1].template pair<E4M3>(j);
-                    const uint32_t w2 = v[u][i][2].template pair<E4M3>(j), w3 = v[u][i][3].template pair<E4M3>(j);
-                    const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-                    const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
+                    uint32_t a0, a1, a2, a3;
+                    row_pairs<E4M3>(v[u][i][0], v[u][i][1], j, a0, a1);
+                    row_pairs<E4M3>(v[u][i][2], v[u][i][3], j, a2, a3);
 #pragma unroll
                     for (int n = 0; n < NT; n++) mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[u][n][0], pb[u][n][1]);
                 }
@@ -540,7 +562,8 @@ struct PagedState {
             }
     }
 
-    // A state in memory: 16 bytes a lane, o's tiles and then m and l.
+    // A state in memory: 16 bytes a lane, each column group's o tiles and then
+    // its m and l.
     __device__ __forceinline__ void save(float *slot, int lane) const
     {
         float4 *p = reinterpret_cast<float4 *>(slot) + lane;
@@ -552,71 +575,79 @@ struct PagedState {
             p[(n * (TILES + 1) + TILES) * 32] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
         }
     }
+};
 
-    // Joins a saved state of other positions: both sides to the larger maximum.
-    __device__ __forceinline__ void join(const float *slot, int lane)
+// One tile of o (16 dims of 8 query heads), with the heads' m and l.
+struct PagedTile {
+    float4 o, ml;
+
+    // Tile i of column group n out of the states that `slot(0)` .. `slot(count
+    // - 1)` hold for different positions: all to the largest maximum, then
+    // added in their order. The loads do not depend on one another.
+    template <class S, class F>
+    __device__ __forceinline__ void gather(int n, int i, int first, int step, int count, int lane, F slot)
     {
-        const float4 *p = reinterpret_cast<const float4 *>(slot) + lane;
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-            const float4 st = p[(n * (TILES + 1) + TILES) * 32];
-            const float mb[2] = {st.x, st.y}, lb[2] = {st.z, st.w};
-            float fa[2], fb[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float top = fmaxf(m[n][e], mb[e]);
-                fa[e] = top == -INFINITY ? 1.0f : ex2_approx(m[n][e] - top);
-                fb[e] = top == -INFINITY ? 1.0f : ex2_approx(mb[e] - top);
-                m[n][e] = top;
-                l[n][e] = l[n][e] * fa[e] + lb[e] * fb[e];
-            }
-#pragma unroll
-            for (int i = 0; i < TILES; i++) {
-                const float4 v = p[(n * (TILES + 1) + i) * 32];
-                o[n][i][0] = o[n][i][0] * fa[0] + v.x * fb[0];
-                o[n][i][1] = o[n][i][1] * fa[1] + v.y * fb[1];
-                o[n][i][2] = o[n][i][2] * fa[0] + v.z * fb[0];
-                o[n][i][3] = o[n][i][3] * fa[1] + v.w * fb[1];
-            }
+        const int at = (n * (S::TILES + 1) + i) * 32 + lane, st = (n * (S::TILES + 1) + S::TILES) * 32 + lane;
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll 8
+        for (int p = first; p < count; p += step) {
+            const float4 s = reinterpret_cast<const float4 *>(slot(p))[st];
+            m0 = fmaxf(m0, s.x), m1 = fmaxf(m1, s.y);
+        }
+        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        ml = make_float4(m0, m1, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int p = first; p < count; p += step) {
+            const float4 *q = reinterpret_cast<const float4 *>(slot(p));
+            const float4 s = q[st], v = q[at];
+            const float f0 = ex2_approx(s.x - b0), f1 = ex2_approx(s.y - b1);
+            ml.z += s.z * f0, ml.w += s.w * f1;
+            o.x += v.x * f0, o.y += v.y * f1, o.z += v.z * f0, o.w += v.w * f1;
         }
     }
 
-    // The states of the CTA's warps joined into warp 0's, halving the warps
-    // that hold one; slots: PA_WARPS / 2 of them in shared memory.
-    __device__ __forceinline__ void join_warps(float *slots, int warp, int lane)
+    // The tile to its place in a saved state.
+    template <class S>
+    __device__ __forceinline__ void save(float *slot, int n, int i, int lane) const
     {
-#pragma unroll
-        for (int w = PA_WARPS / 2; w >= 1; w >>= 1) {
-            if (warp >= w && warp < 2 * w) save(slots + (warp - w) * SLOT, lane);
-            __syncthreads();
-            if (warp < w) join(slots + warp * SLOT, lane);
-            __syncthreads();
-        }
+        float4 *p = reinterpret_cast<float4 *>(slot) + lane;
+        p[(n * (S::TILES + 1) + i) * 32] = o;
+        if (i == 0) p[(n * (S::TILES + 1) + S::TILES) * 32] = ml;
     }
 
-    // out and lse of the heads from `head` on, of which `heads` are live.
-    template <typename QT>
-    __device__ __forceinline__ void store(uint16_t *out, float *lse, int heads, float v_scale, int lane) const
+    // The tile's part of out and (tile 0) lse, of `heads` live heads.
+    template <class S, typename QT>
+    __device__ __forceinline__ void store(uint16_t *out, float *lse, int heads, float v_scale, int n, int i, int lane) const
     {
         const int g = lane >> 2, t = lane & 3;
+        const int d = (i / S::VJ) * 8 * S::VD + g * S::VD + 2 * (i % S::VJ);
 #pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const int h = n * 8 + 2 * t + e;
-                if (h >= heads) continue;
-                const float inv = l[n][e] == 0.0f ? 0.0f : v_scale / l[n][e];
-                uint16_t *dst = out + (long long)h * D;
-#pragma unroll
-                for (int i = 0; i < VI; i++)
-#pragma unroll
-                    for (int j = 0; j < VJ; j++)
-                        *reinterpret_cast<uint32_t *>(dst + i * 8 * VD + g * VD + 2 * j) =
-                            from_f2<QT>(o[n][i * VJ + j][e] * inv, o[n][i * VJ + j][2 + e] * inv);
-                if (lse && g == 0) lse[h] = (m[n][e] + log2f(l[n][e])) * 0.69314718055994531f;
-            }
+        for (int e = 0; e < 2; e++) {
+            const int h = n * 8 + 2 * t + e;
+            if (h >= heads) continue;
+            const float l = e ? ml.w : ml.z, inv = l == 0.0f ? 0.0f : v_scale / l;
+            *reinterpret_cast<uint32_t *>(out + (long long)h * S::DIM + d) =
+                from_f2<QT>((e ? o.y : o.x) * inv, (e ? o.w : o.z) * inv);
+            if (lse && g == 0 && i == 0) lse[h] = ((e ? ml.y : ml.x) + log2f(l)) * 0.69314718055994531f;
+        }
     }
 };
+
+// The states of the CTA's warps through shared memory (one slot a warp), each
+// warp joining its tiles: done(tile, n, i).
+template <class S, class F>
+__device__ __forceinline__ void warps_join(const S &st, float *slots, int warp, int lane, F done)
+{
+    __syncthreads();  // the slots are free
+    st.save(slots + warp * S::SLOT, lane);
+    __syncthreads();
+    for (int x = warp; x < S::COLUMNS * S::TILES; x += PA_WARPS) {
+        PagedTile t;
+        t.template gather<S>(x / S::TILES, x % S::TILES, 0, 1, PA_WARPS, lane, [&](int w) { return slots + w * S::SLOT; });
+        done(t, x / S::TILES, x % S::TILES);
+    }
+}
 
 // The work of a launch is a row of tiles, in the order
 // (sequence, key head and group of query heads, tile): the lengths are only
@@ -728,15 +759,15 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
             st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f),
                                    lane);
             st.run(a.c, s, head, tile * S::TILE, min(len, last * S::TILE), warp, lane);
-            st.join_warps(pa_slots, warp, lane);
-            if (warp == 0) {
-                if (tile == 0 && last == tiles)
-                    st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D,
-                                          a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
-                                          E4M3 ? a.c.v_scale : 1.0f, lane);
+            const bool whole = tile == 0 && last == tiles;
+            float *piece = pieces + (2ll * blockIdx.x + (tile == 0)) * S::SLOT;
+            warps_join(st, pa_slots, warp, lane, [&](const PagedTile &x, int n, int i) {
+                if (whole)
+                    x.template store<S, QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr,
+                                            heads, E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
                 else
-                    st.save(pieces + (2ll * blockIdx.x + (tile == 0)) * S::SLOT, lane);
-            }
+                    x.template save<S>(piece, n, i, lane);
+            });
             if (tile == 0 && last < tiles) split = {s, unit, (int)((tiles - last + sh.share - 1) / sh.share)};
             sh.count -= last - tile;
         }
@@ -762,35 +793,54 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
     st.clear();
     st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
     st.run(a.c, s, head, 0, len, warp, lane);
-    st.join_warps(pa_slots, warp, lane);
-    if (warp == 0)
-        st.template store<QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr,
-                              heads, E4M3 ? a.c.v_scale : 1.0f, lane);
+    warps_join(st, pa_slots, warp, lane, [&](const PagedTile &x, int n, int i) {
+        x.template store<S, QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
+                                E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
+    });
 }
 
 // CTA i joins the unit that was split from share i on: its first piece is the
-// share's second, the others are the first pieces of the next shares.
+// share's second, the others are the first pieces of the next shares. A warp
+// has one tile and every PJ_PARTS-th piece.
+static constexpr int PJ_PARTS = 2;
+
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(32 * PA_WARPS) paged_join_kernel(PagedAttnArgs a, const float *pieces, const PagedSplit *splits)
+__global__ void __launch_bounds__(2 * D * NT * PJ_PARTS) paged_join_kernel(PagedAttnArgs a, const float *pieces,
+                                                                           const PagedSplit *splits)
 {
     using S = PagedState<T, E4M3, D, NT>;
-    extern __shared__ __align__(16) float pa_slots[];
+    __shared__ float4 part[PJ_PARTS][S::TILES * NT][2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int x = warp % (S::TILES * NT), sub = warp / (S::TILES * NT), n = x / S::TILES, i = x % S::TILES;
     grid_dep_wait();
     grid_dep_launch();
     PagedSplit sp = splits[blockIdx.x];
     if (sp.pieces == 0) return;
     sp.pieces = min(sp.pieces, (int)(gridDim.x - 1 - blockIdx.x));
-    S st;
-    st.clear();
-    for (int i = warp; i <= sp.pieces; i += PA_WARPS)
-        st.join(pieces + (2ll * (blockIdx.x + i) + (i == 0)) * S::SLOT, lane);
-    st.join_warps(pa_slots, warp, lane);
-    if (warp != 0) return;
+    PagedTile t;
+    t.template gather<S>(n, i, sub, PJ_PARTS, sp.pieces + 1, lane,
+                         [&](int p) { return pieces + (2ll * (blockIdx.x + p) + (p == 0)) * S::SLOT; });
+    part[sub][x][0][lane] = t.o;
+    part[sub][x][1][lane] = t.ml;
+    __syncthreads();
+    if (sub != 0) return;
+    float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+    for (int p = 0; p < PJ_PARTS; p++) m0 = fmaxf(m0, part[p][x][1][lane].x), m1 = fmaxf(m1, part[p][x][1][lane].y);
+    const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+    t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    t.ml = make_float4(m0, m1, 0.0f, 0.0f);
+#pragma unroll
+    for (int p = 0; p < PJ_PARTS; p++) {
+        const float4 v = part[p][x][0][lane], s = part[p][x][1][lane];
+        const float f0 = ex2_approx(s.x - b0), f1 = ex2_approx(s.y - b1);
+        t.ml.z += s.z * f0, t.ml.w += s.w * f1;
+        t.o.x += v.x * f0, t.o.y += v.y * f1, t.o.z += v.z * f0, t.o.w += v.w * f1;
+    }
     const int head = sp.unit / a.head_groups, hg = sp.unit - head * a.head_groups;
     const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
-    st.template store<QT>(a.out + ((long long)sp.s * a.hq + h0) * D, a.lse ? a.lse + (long long)sp.s * a.hq + h0 : nullptr,
-                          heads, E4M3 ? a.c.v_scale : 1.0f, lane);
+    t.template store<S, QT>(a.out + ((long long)sp.s * a.hq + h0) * D, a.lse ? a.lse + (long long)sp.s * a.hq + h0 : nullptr, heads,
+                            E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
 }
 
 }  // namespace moss

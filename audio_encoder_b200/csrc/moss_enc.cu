@@ -2812,8 +2812,12 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
                                       double bytes)
 {
     using S = PagedState<T, E4M3, D, NT>;
-    constexpr size_t smem = sizeof(float) * S::SLOT * (PA_WARPS / 2);
-    static_assert(smem <= 48 * 1024, "no attribute needed for the joined states");
+    constexpr size_t smem = sizeof(float) * S::SLOT * PA_WARPS;
+    static_assert(smem <= SMEM_LIMIT, "the warps' states fit shared memory");
+    if constexpr (smem > 48 * 1024) {
+        CUDA_TRY(h, cudaFuncSetAttribute(paged_attn_units_kernel<T, QT, E4M3, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        CUDA_TRY(h, cudaFuncSetAttribute(paged_attn_kernel<T, QT, E4M3, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    }
     const dim3 grid((unsigned)g.ctas), block(32 * PA_WARPS);
     if (!g.split) {
         Launch L(h, "paged_attn", flops, bytes);
@@ -2827,7 +2831,7 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
         CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, pieces, splits));
     }
     Launch L(h, "paged_join", 0, 0);
-    CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, (const float *)pieces,
+    CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, grid, dim3(2 * D * NT * PJ_PARTS), 0, a, (const float *)pieces,
                          (const PagedSplit *)splits));
     return MOSS_ENC_OK;
 }
