@@ -35,14 +35,18 @@ struct PagedKV {
     {
         return page * stride_page + (pos & ((1 << page_shift) - 1)) * stride_token;
     }
-    // The page that holds position pos of sequence s, or -1 with the error
-    // word set when the table names a page that the cache does not have.
-    __device__ __forceinline__ int page_of(int s, int pos) const
+    // What the table says of the page that holds position pos of sequence s
+    // (0 past the table).
+    __device__ __forceinline__ int entry(int s, int pos) const
     {
-        const int p = table[s * table_stride + (pos >> page_shift)];
-        if ((unsigned)p < (unsigned)n_pages) return p;
+        return (pos >> page_shift) < pages_per_seq ? table[s * table_stride + (pos >> page_shift)] : 0;
+    }
+    // Whether the cache has such a page; the error word is set if not.
+    __device__ __forceinline__ bool has(int page) const
+    {
+        if ((unsigned)page < (unsigned)n_pages) return true;
         atomicOr(flag, DEV_ERR_PAGE);
-        return -1;
+        return false;
     }
 };
 
@@ -134,11 +138,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
     if (seq < 0) return;  // a padding row: nothing is written
     const int pos = a.positions[row];
     int page = -1;
-    if (seq < a.c.n_seqs && pos >= 0 && (pos >> a.c.page_shift) < a.c.pages_per_seq)
-        page = a.c.page_of(seq, pos);
-    else if (tid == 0)
-        atomicOr(a.c.flag, DEV_ERR_PAGE);
-    if (page < 0) return;
+    if (seq < a.c.n_seqs && pos >= 0 && (pos >> a.c.page_shift) < a.c.pages_per_seq) page = a.c.entry(seq, pos);
+    if (!a.c.has(page)) return;
 
     for (int i = tid; i < a.rotary / 2; i += blockDim.x) {
         const double turns = (double)pos * a.inv_freq[i] * 0.15915494309189533577;
@@ -540,18 +541,32 @@ struct PagedState {
                 }
     }
 
-    // Positions [t0, end) of one key head of sequence s, by the CTA's warps in
-    // turn.
-    __device__ __forceinline__ void run(const PagedKV &c, int s, int head, int t0, int end, int warp, int lane)
+    // The table's entries for a step at p0. They may be asked for before the
+    // sequence's length is known; what lies past it is not looked at.
+    __device__ __forceinline__ static void pages(const PagedKV &c, int s, int p0, int (&page)[SUB])
     {
-        for (int p0 = t0 + 16 * SUB * warp; p0 < end; p0 += TILE) {
+#pragma unroll
+        for (int u = 0; u < SUB; u++) page[u] = c.entry(s, p0 + 16 * u);
+    }
+
+    // Positions p0, p0 + stride, ... below `end`, a step at each, of one key
+    // head of sequence s; `page`: the table's entries for the first. Each
+    // step's entries are read a step ahead.
+    __device__ __forceinline__ void run(const PagedKV &c, int s, int head, int p0, int stride, int end, int (&page)[SUB], int lane)
+    {
+        while (p0 < end) {
             long long off[SUB];
 #pragma unroll
             for (int u = 0; u < SUB; u++) {
-                const int p = min(p0 + 16 * u, (end - 1) & ~15);
-                off[u] = c.at(max(c.page_of(s, p), 0), p) + head * c.stride_head;
+                if (u == 0 || p0 + 16 * u < end)
+                    off[u] = c.at(c.has(page[u]) ? page[u] : 0, p0 + 16 * u) + head * c.stride_head;
+                else
+                    off[u] = off[u > 0 ? u - 1 : 0];
             }
-            step(c, off, p0, end, lane);
+            const int at = p0;
+            p0 += stride;
+            if (p0 < end) pages(c, s, p0, page);
+            step(c, off, at, end, lane);
         }
 #pragma unroll
         for (int n = 0; n < NT; n++)
@@ -755,10 +770,13 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
             const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
             const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
             const int last = (int)min((long long)tiles, tile + sh.count);
+            int page[S::SUB];
+            const int p0 = tile * S::TILE + 16 * S::SUB * warp;
+            S::pages(a.c, s, p0, page);
             st.clear();
             st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f),
                                    lane);
-            st.run(a.c, s, head, tile * S::TILE, min(len, last * S::TILE), warp, lane);
+            st.run(a.c, s, head, p0, S::TILE, min(len, last * S::TILE), page, lane);
             const bool whole = tile == 0 && last == tiles;
             float *piece = pieces + (2ll * blockIdx.x + (tile == 0)) * S::SLOT;
             warps_join(st, pa_slots, warp, lane, [&](const PagedTile &x, int n, int i) {
@@ -775,28 +793,54 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
     if (tid == 0) splits[blockIdx.x] = split;
 }
 
-// One CTA per unit, for lengths that are not worth splitting.
+// The address of `p` (this CTA's shared memory) in the cluster's CTA `rank`.
+__device__ __forceinline__ float *cluster_slot(float *p, uint32_t rank)
+{
+    uint64_t r;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(rank));
+    return reinterpret_cast<float *>(r);
+}
+
+// One cluster per unit, for lengths that a few steps of its CTAs take: they
+// read its tiles in turn, and join through one another's shared memory, so
+// there is neither a workspace nor a second launch. `ways`: CTAs of a cluster.
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_units_kernel(PagedAttnArgs a)
+__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_unit_kernel(PagedAttnArgs a, int ways)
 {
     using S = PagedState<T, E4M3, D, NT>;
     extern __shared__ __align__(16) float pa_slots[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int units = a.c.hkv * a.head_groups;
-    const int s = blockIdx.x / units, unit = blockIdx.x - s * units;
+    const int units = a.c.hkv * a.head_groups, rank = blockIdx.x % ways, which = blockIdx.x / ways;
+    const int s = which / units, unit = which - s * units;
     const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
     const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    const int p0 = rank * S::TILE + 16 * S::SUB * warp;
     grid_dep_wait();
     grid_dep_launch();
+    int page[S::SUB];
+    S::pages(a.c, s, p0, page);
     const int len = paged_len(a, s, threadIdx.x == 0);
     S st;
     st.clear();
     st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
-    st.run(a.c, s, head, 0, len, warp, lane);
-    warps_join(st, pa_slots, warp, lane, [&](const PagedTile &x, int n, int i) {
+    st.run(a.c, s, head, p0, ways * S::TILE, len, page, lane);
+    const auto store = [&](const PagedTile &x, int n, int i) {
         x.template store<S, QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
                                 E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
-    });
+    };
+    if (ways == 1) {
+        warps_join(st, pa_slots, warp, lane, store);
+        return;
+    }
+    float *mine = pa_slots + PA_WARPS * S::SLOT;
+    warps_join(st, pa_slots, warp, lane, [&](const PagedTile &x, int n, int i) { x.template save<S>(mine, n, i, lane); });
+    cluster_sync_all();
+    for (int x = warp * ways + rank; x < NT * S::TILES; x += PA_WARPS * ways) {
+        PagedTile t;
+        t.template gather<S>(x / S::TILES, x % S::TILES, 0, 1, ways, lane, [&](int r) { return cluster_slot(mine, r); });
+        store(t, x / S::TILES, x % S::TILES);
+    }
+    cluster_sync_all();  // nobody leaves while its slot is read
 }
 
 // CTA i joins the unit that was split from share i on: its first piece is the

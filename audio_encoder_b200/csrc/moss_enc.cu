@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <thread>
@@ -183,21 +184,32 @@ struct Launch {
 // programmatic stream serialisation: the kernel may start while the previous
 // one finishes, and waits for it (griddepcontrol.wait) before touching its
 // results; every kernel launched here does so.
+// cluster: CTAs of a cluster (1: none, or what the kernel itself declares).
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_k(moss_enc *h, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, Args... args)
+static cudaError_t launch_cluster(moss_enc *h, void (*kern)(KArgs...), int cluster, dim3 grid, dim3 block, size_t smem,
+                                  Args... args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = h->stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = h->pdl && !h->pdl_skip_once ? 1 : 0;
     h->pdl_skip_once = false;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_k(moss_enc *h, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, Args... args)
+{
+    return launch_cluster(h, kern, 1, grid, block, smem, args...);
 }
 
 static moss_enc_status fail(moss_enc *h, moss_enc_status s, const std::string &msg)
@@ -2622,7 +2634,7 @@ static const char *cache_refusal(const moss_enc_kv_cache *c)
     if (c->n_seqs < 0 || c->n_kv_heads < 1 || c->n_kv_heads > 65535 || c->n_pages < 1 || c->pages_per_seq < 1)
         return "n_seqs, n_kv_heads, n_pages or pages_per_seq out of range";
     if (c->page_size < 16 || (c->page_size & (c->page_size - 1)) != 0) return "page_size must be a power of two, 16 or more";
-    if ((int64_t)c->page_size * c->pages_per_seq > INT32_MAX) return "a sequence's pages hold 2^31 positions or more";
+    if ((int64_t)c->page_size * c->pages_per_seq > (1 << 30)) return "a sequence's pages hold more than 2^30 positions";
     if (!c->k || !c->v || (!c->page_table && c->n_seqs > 0) || !aligned(c->k, 16) || !aligned(c->v, 16) ||
         !aligned(c->page_table, 4))
         return "k and v must be 16-byte aligned, page_table 4-byte";
@@ -2767,13 +2779,15 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 // head_dim 256 does not leave).
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
-// The launch of paged_attn: one CTA per unit (a sequence's key head), or
-// shares of tiles that may split units and a join after it.  Up to
-// ATTN_WHOLE positions a unit is left whole.
-constexpr int ATTN_WHOLE = 512;
+// The launch of paged_attn. A unit is a sequence's key head with up to 8 or 16
+// of its query heads. While units are few, a cluster of `ways` CTAs takes
+// each, if that leaves its CTAs ATTN_STEPS tiles at most; otherwise the tiles
+// of all units are dealt out evenly, with a join after (split).
+constexpr int ATTN_STEPS = 6, ATTN_WAYS = 16;
 
 struct AttnGrid {
     int64_t ctas;
+    int ways;
     bool split;
 };
 
@@ -2783,10 +2797,13 @@ static AttnGrid attn_grid(const moss_enc *h, const moss_enc_kv_cache *c, int gro
     const int64_t cap = (int64_t)c->page_size * c->pages_per_seq;
     const int64_t bound = max_len > 0 ? std::min<int64_t>(max_len, cap) : cap;
     const int tile = pa_tile(c->head_dim, c->dtype == MOSS_ENC_KV_E4M3);
+    const int64_t tiles = (bound + tile - 1) / tile;
     const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * head_groups;
-    if (bound <= ATTN_WHOLE) return AttnGrid{units, false};
     const int resident = h->num_sms * (c->head_dim <= 128 && columns == 1 ? 2 : 1);
-    return AttnGrid{std::max<int64_t>(1, std::min<int64_t>(units * ((bound + tile - 1) / tile), resident)), true};
+    int ways = 1;
+    while (ways < ATTN_WAYS && ways < tiles && units * ways * 2 <= resident) ways *= 2;
+    if (tiles <= (int64_t)ATTN_STEPS * ways && units * ways <= INT32_MAX) return AttnGrid{units * ways, ways, false};
+    return AttnGrid{std::min<int64_t>(units * tiles, resident), 1, true};
 }
 
 // Bytes of one saved state: 8 columns' sums, maxima and outputs.
@@ -2807,23 +2824,36 @@ extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_e
     return attn_workspace(h, cache, n_q_heads / cache->n_kv_heads, max_len);
 }
 
+// A kernel's attributes, once per device (`done`: a bit for each).
+template <class K>
+static cudaError_t attn_attrs(const moss_enc *h, std::atomic<uint64_t> &done, K *kern, size_t smem, bool clusters)
+{
+    const uint64_t bit = h->device < 64 ? uint64_t(1) << h->device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 template <typename T, typename QT, bool E4M3, int D, int NT>
 static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const AttnGrid &g, void *workspace, double flops,
                                       double bytes)
 {
     using S = PagedState<T, E4M3, D, NT>;
-    constexpr size_t smem = sizeof(float) * S::SLOT * PA_WARPS;
-    static_assert(smem <= SMEM_LIMIT, "the warps' states fit shared memory");
-    if constexpr (smem > 48 * 1024) {
-        CUDA_TRY(h, cudaFuncSetAttribute(paged_attn_units_kernel<T, QT, E4M3, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-        CUDA_TRY(h, cudaFuncSetAttribute(paged_attn_kernel<T, QT, E4M3, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    }
+    constexpr size_t smem = sizeof(float) * S::SLOT * PA_WARPS, smem_ways = smem + sizeof(float) * S::SLOT;
+    static_assert(smem_ways <= SMEM_LIMIT, "the warps' states fit shared memory");
     const dim3 grid((unsigned)g.ctas), block(32 * PA_WARPS);
     if (!g.split) {
+        const auto kern = paged_attn_unit_kernel<T, QT, E4M3, D, NT>;
+        static std::atomic<uint64_t> done{0};
+        CUDA_TRY(h, attn_attrs(h, done, kern, smem_ways, true));
         Launch L(h, "paged_attn", flops, bytes);
-        CUDA_TRY(h, launch_k(h, paged_attn_units_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a));
+        CUDA_TRY(h, launch_cluster(h, kern, g.ways, grid, block, g.ways > 1 ? smem_ways : smem, a, g.ways));
         return MOSS_ENC_OK;
     }
+    static std::atomic<uint64_t> done{0};
+    CUDA_TRY(h, attn_attrs(h, done, paged_attn_kernel<T, QT, E4M3, D, NT>, smem, false));
     float *pieces = static_cast<float *>(workspace);
     PagedSplit *splits = reinterpret_cast<PagedSplit *>(pieces + (size_t)g.ctas * 2 * S::SLOT);
     {

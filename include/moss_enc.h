@@ -434,7 +434,7 @@ enum { MOSS_ENC_KV_BF16 = 0, MOSS_ENC_KV_F16 = 1, MOSS_ENC_KV_E4M3 = 2 };
  *             page i of a sequence holds its positions i * page_size ...
  *             Entries past a sequence's last position are not read.
  *  page_size  a power of two, 16 or more; n_pages >= 1; pages_per_seq >= 1 and
- *             pages_per_seq * page_size < 2^31.
+ *             pages_per_seq * page_size <= 2^30.
  *  head_dim   64, 128 or 256.
  *  dtype      MOSS_ENC_KV_*.  An e4m3 cache holds keys / k_scale and values /
  *             v_scale (finite, > 0; not used by the 16-bit types), rounded to

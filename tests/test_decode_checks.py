@@ -46,7 +46,7 @@ def test_plain_arguments_are_taken():
 @pytest.mark.parametrize("kw", [
     dict(dtype=3), dict(dtype=-1), dict(head_dim=96), dict(head_dim=0), dict(n_seqs=-1), dict(n_kv_heads=0),
     dict(n_pages=0), dict(pages_per_seq=0), dict(page_size=8), dict(page_size=48), dict(page_size=0),
-    dict(page_size=1 << 20, pages_per_seq=1 << 11), dict(k=None), dict(v=None), dict(page_table=None), dict(k=P + 8),
+    dict(page_size=1 << 20, pages_per_seq=(1 << 10) + 1, table_stride=1 << 11), dict(k=None), dict(v=None), dict(page_table=None), dict(k=P + 8),
     dict(v=P + 2), dict(page_table=P + 2), dict(stride_token=1028), dict(stride_token=64), dict(stride_head=64),
     dict(stride_head=132), dict(stride_page=-2048), dict(stride_page=4), dict(stride_page=1 << 59), dict(stride_token=1 << 58), dict(table_stride=3),
     dict(dtype=binding.KV_E4M3, k_scale=0.0), dict(dtype=binding.KV_E4M3, v_scale=-1.0),
@@ -59,7 +59,7 @@ def test_caches_that_are_refused(kw):
 @pytest.mark.parametrize("kw", [
     dict(n_seqs=0, page_table=None), dict(n_pages=1, stride_page=0), dict(stride_page=1 << 40), dict(n_kv_heads=1, stride_head=0),
     dict(n_seqs=1, table_stride=0), dict(k_scale=0.0), dict(dtype=binding.KV_E4M3, k_scale=0.5),
-    dict(stride_token=128, stride_head=16 * 128), dict(page_size=1 << 20, pages_per_seq=(1 << 11) - 1, table_stride=1 << 11)])
+    dict(stride_token=128, stride_head=16 * 128), dict(page_size=1 << 20, pages_per_seq=1 << 10, table_stride=1 << 11)])
 def test_caches_that_are_taken(kw):
     assert refusal(cache(**kw)) is None
 

@@ -459,7 +459,8 @@ def test_paged_attn_pages_and_layouts(enc, page, layout):
 
 
 @pytest.mark.parametrize("ct", [BF16, F16, E4M3])
-@pytest.mark.parametrize("lengths", [[9000], [45000], [20000, 3], [4097, 0, 4096, 4095, 1, 12345]])
+@pytest.mark.parametrize("lengths", [[1500], [9000], [45000], [20000, 3], [4097, 0, 4096, 4095, 1, 12345], [130000],
+                                     [0] * 70 + [9000, 0, 2500] + [1100] * 50])
 def test_paged_attn_long(enc, ct, lengths):
     g = gen(sum(lengths))
     cache = make_cache(len(lengths), max(lengths), 64, 2, 128, ct, g)
@@ -567,24 +568,24 @@ def test_paged_attn_bound_on_the_lengths(enc):
     lengths = [100, 3000, 0, 17]
     cache = make_cache(4, 4000, 16, 2, 128, BF16, g)
     q = randn((4, 4, 128), g, BF16, 2.0)
-    for bound in (0, 1, 100, 3000, 1 << 30):
+    for bound in (0, 1, 100, 1000, 3000, 1 << 30):
         check_attn(enc, cache, q, lengths, max_len=bound)
 
 
 def test_paged_attn_refuses_a_workspace_that_is_too_small(enc):
     g = gen(64)
-    cache = make_cache(2, 3000, 16, 2, 64, BF16, g)
+    cache = make_cache(2, 60000, 16, 2, 64, BF16, g)
     q = randn((2, 4, 64), g, BF16)
-    n = torch.tensor([3000, 6], dtype=torch.int32, device="cuda")
+    n = torch.tensor([60000, 6], dtype=torch.int32, device="cuda")
     need = enc.paged_attn_workspace(cache, 4)
     assert need > 0
     big = torch.empty(need + 16, dtype=torch.uint8, device="cuda")
     for bad in (big[:need - 1], big[8:8 + need], big[::2], big.view(torch.int8)):
         with pytest.raises((ValueError, binding.MossEncError)):
             enc.paged_attn(cache, q, n, workspace=bad)
-    check_attn(enc, cache, q, [3000, 6], workspace=big)
-    short = make_cache(2, 100, 16, 2, 64, BF16, g)
-    assert enc.paged_attn_workspace(short, 4) == 0 and enc.paged_attn_workspace(cache, 4, max_len=100) == 0
+    check_attn(enc, cache, q, [60000, 6], workspace=big)
+    n_short = make_cache(2, 100, 16, 2, 64, BF16, g)
+    assert enc.paged_attn_workspace(n_short, 4) == 0 and enc.paged_attn_workspace(cache, 4, max_len=100) == 0
 
 
 def test_paged_attn_reports_lengths_and_pages_outside_the_cache(enc):
@@ -704,7 +705,7 @@ def test_decoding_step_on_another_stream_and_in_graphs():
     s0, s1 = torch.cuda.Stream(), torch.cuda.Stream()
     e = binding.Encoder(weights(1), 1, max_samples=16000, max_clips=1)
     sets = []
-    for stream, longest in ((s0, 9000), (s1, 5000)):
+    for stream, longest in ((s0, 90000), (s1, 50000)):
         cache, qkv, proj, inv, dims = step_setup(g, 3, longest)
         n = torch.tensor([longest - 50, 700, 1], dtype=torch.int32, device="cuda")
         x = randn((3, dims[3]), g, BF16)
