@@ -596,29 +596,40 @@ struct PagedState {
 struct PagedTile {
     float4 o, ml;
 
-    // Tile i of column group n out of the states that `slot(0)` .. `slot(count
-    // - 1)` hold for different positions: all to the largest maximum, then
-    // added in their order. The loads do not depend on one another.
+    // Tile i of column group n out of the states that slot(first), slot(first +
+    // step) ... below `count` hold for different positions: eight at a time to
+    // the largest maximum so far, then added in their order.
     template <class S, class F>
     __device__ __forceinline__ void gather(int n, int i, int first, int step, int count, int lane, F slot)
     {
         const int at = (n * (S::TILES + 1) + i) * 32 + lane, st = (n * (S::TILES + 1) + S::TILES) * 32 + lane;
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll 8
-        for (int p = first; p < count; p += step) {
-            const float4 s = reinterpret_cast<const float4 *>(slot(p))[st];
-            m0 = fmaxf(m0, s.x), m1 = fmaxf(m1, s.y);
-        }
-        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
         o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        ml = make_float4(m0, m1, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int p = first; p < count; p += step) {
-            const float4 *q = reinterpret_cast<const float4 *>(slot(p));
-            const float4 s = q[st], v = q[at];
-            const float f0 = ex2_approx(s.x - b0), f1 = ex2_approx(s.y - b1);
-            ml.z += s.z * f0, ml.w += s.w * f1;
-            o.x += v.x * f0, o.y += v.y * f1, o.z += v.z * f0, o.w += v.w * f1;
+        ml = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+        for (; first < count; first += 8 * step) {
+            float4 s[8], v[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int p = first + k * step;
+                s[k] = make_float4(-INFINITY, -INFINITY, 0.0f, 0.0f);
+                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (p < count) {
+                    const float4 *q = reinterpret_cast<const float4 *>(slot(p));
+                    s[k] = q[st], v[k] = q[at];
+                }
+            }
+            float m0 = ml.x, m1 = ml.y;
+#pragma unroll
+            for (int k = 0; k < 8; k++) m0 = fmaxf(m0, s[k].x), m1 = fmaxf(m1, s[k].y);
+            const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+            const float f0 = ex2_approx(ml.x - b0), f1 = ex2_approx(ml.y - b1);
+            ml = make_float4(m0, m1, ml.z * f0, ml.w * f1);
+            o = make_float4(o.x * f0, o.y * f1, o.z * f0, o.w * f1);
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const float e0 = ex2_approx(s[k].x - b0), e1 = ex2_approx(s[k].y - b1);
+                ml.z += s[k].z * e0, ml.w += s[k].w * e1;
+                o.x += v[k].x * e0, o.y += v[k].y * e1, o.z += v[k].z * e0, o.w += v[k].w * e1;
+            }
         }
     }
 
@@ -670,10 +681,6 @@ __device__ __forceinline__ void warps_join(const S &st, float *slots, int warp, 
 // the tiles. A share may end inside a unit (one sequence's key head); then the
 // unit's pieces go to the workspace and paged_join_kernel puts them together,
 // in the order of the positions, so results do not depend on timing.
-struct PagedSplit {
-    int s, unit, pieces;  // the unit that starts in this CTA's share and goes on in the next `pieces` shares
-};
-
 // Where a CTA's share starts.
 struct PagedShare {
     long long first, count;  // tiles
@@ -690,16 +697,16 @@ __device__ __forceinline__ int paged_len(const PagedAttnArgs &a, int s, bool rep
     return min(max(len, 0), cap);
 }
 
-// Thread i of the CTA adds up the tiles of its span of the sequences; a scan
-// over the spans gives the total and the span in which this CTA's share
-// starts, whose thread walks it.
-template <int TILE>
+// Thread i of the CTA's WARPS warps adds up the tiles of its span of the
+// sequences; a scan over the spans gives the total and the span in which this
+// CTA's share starts, whose thread walks it.
+template <int TILE, int WARPS>
 __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int units)
 {
-    __shared__ long long warp_sums[PA_WARPS];
+    __shared__ long long warp_sums[WARPS];
     __shared__ long long found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int span = (a.c.n_seqs + 32 * PA_WARPS - 1) / (32 * PA_WARPS);
+    const int span = (a.c.n_seqs + 32 * WARPS - 1) / (32 * WARPS);
     const int lo = min(tid * span, a.c.n_seqs), hi = min(lo + span, a.c.n_seqs);
     long long mine = 0;
     for (int s = lo; s < hi; s++) mine += (long long)((paged_len(a, s, blockIdx.x == 0) + TILE - 1) / TILE) * units;
@@ -714,7 +721,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
     __syncthreads();
     long long total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < PA_WARPS; w++) {
+    for (int w = 0; w < WARPS; w++) {
         if (w < warp) before += warp_sums[w];
         total += warp_sums[w];
     }
@@ -741,8 +748,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
 }
 
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a, float *pieces,
-                                                                                           PagedSplit *splits)
+__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_kernel(PagedAttnArgs a, float *pieces)
 {
     using S = PagedState<T, E4M3, D, NT>;
     extern __shared__ __align__(16) float pa_slots[];
@@ -750,8 +756,7 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
     const int units = a.c.hkv * a.head_groups;
     grid_dep_wait();
     grid_dep_launch();
-    PagedShare sh = paged_share<S::TILE>(a, units);
-    PagedSplit split = {0, 0, 0};
+    PagedShare sh = paged_share<S::TILE, PA_WARPS>(a, units);
 
     // sequences without a position: nobody's share
     for (int s = blockIdx.x; s < a.c.n_seqs; s += gridDim.x)
@@ -786,11 +791,9 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
                 else
                     x.template save<S>(piece, n, i, lane);
             });
-            if (tile == 0 && last < tiles) split = {s, unit, (int)((tiles - last + sh.share - 1) / sh.share)};
             sh.count -= last - tile;
         }
     }
-    if (tid == 0) splits[blockIdx.x] = split;
 }
 
 // The address of `p` (this CTA's shared memory) in the cluster's CTA `rank`.
@@ -845,24 +848,44 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
 
 // CTA i joins the unit that was split from share i on: its first piece is the
 // share's second, the others are the first pieces of the next shares. A warp
-// has one tile and every PJ_PARTS-th piece.
-static constexpr int PJ_PARTS = 2;
+// has one tile and every PARTS-th piece. Which unit that is follows from
+// the lengths, so it is worked out before the pieces are waited for (the
+// lengths are older than the kernel that writes the pieces, which lets this
+// one start only when they are there).
+__host__ __device__ constexpr int pj_parts(int dim, int columns) { return dim * columns >= 256 ? 1 : 2; }
 
 template <typename T, typename QT, bool E4M3, int D, int NT>
-__global__ void __launch_bounds__(2 * D * NT * PJ_PARTS) paged_join_kernel(PagedAttnArgs a, const float *pieces,
-                                                                           const PagedSplit *splits)
+__global__ void __launch_bounds__(2 * D * NT * pj_parts(D, NT)) paged_join_kernel(PagedAttnArgs a, const float *pieces)
 {
     using S = PagedState<T, E4M3, D, NT>;
-    __shared__ float4 part[PJ_PARTS][S::TILES * NT][2][32];
+    constexpr int PARTS = pj_parts(D, NT);
+    __shared__ float4 part[PARTS][S::TILES * NT][2][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int x = warp % (S::TILES * NT), sub = warp / (S::TILES * NT), n = x / S::TILES, i = x % S::TILES;
+    const int units = a.c.hkv * a.head_groups;
+    PagedShare sh = paged_share<S::TILE, S::TILES * NT * PARTS>(a, units);
+    // the last unit of the share, and its tiles past the share's end
+    int s = sh.s, unit = 0;
+    long long left = 0;
+    if (sh.count > 0 && s < a.c.n_seqs) {
+        long long end = sh.offset + sh.count;  // the share's end, in tiles from sequence s's start
+        int tiles;
+        for (;; s++) {
+            tiles = (paged_len(a, s, false) + S::TILE - 1) / S::TILE;
+            if (end <= (long long)tiles * units || s + 1 >= a.c.n_seqs) break;
+            end -= (long long)tiles * units;
+            sh.offset -= (long long)tiles * units;
+        }
+        unit = tiles > 0 ? (int)((end - 1) / tiles) : 0;
+        const long long starts = (long long)unit * tiles;
+        if (starts >= sh.offset) left = starts + tiles - end;  // else it began in an earlier share
+    }
+    const int more = (int)min((left + sh.share - 1) / sh.share, (long long)(gridDim.x - 1 - blockIdx.x));
     grid_dep_wait();
     grid_dep_launch();
-    PagedSplit sp = splits[blockIdx.x];
-    if (sp.pieces == 0) return;
-    sp.pieces = min(sp.pieces, (int)(gridDim.x - 1 - blockIdx.x));
+    if (more <= 0) return;
     PagedTile t;
-    t.template gather<S>(n, i, sub, PJ_PARTS, sp.pieces + 1, lane,
+    t.template gather<S>(n, i, sub, PARTS, more + 1, lane,
                          [&](int p) { return pieces + (2ll * (blockIdx.x + p) + (p == 0)) * S::SLOT; });
     part[sub][x][0][lane] = t.o;
     part[sub][x][1][lane] = t.ml;
@@ -870,20 +893,20 @@ __global__ void __launch_bounds__(2 * D * NT * PJ_PARTS) paged_join_kernel(Paged
     if (sub != 0) return;
     float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-    for (int p = 0; p < PJ_PARTS; p++) m0 = fmaxf(m0, part[p][x][1][lane].x), m1 = fmaxf(m1, part[p][x][1][lane].y);
+    for (int p = 0; p < PARTS; p++) m0 = fmaxf(m0, part[p][x][1][lane].x), m1 = fmaxf(m1, part[p][x][1][lane].y);
     const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
     t.o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     t.ml = make_float4(m0, m1, 0.0f, 0.0f);
 #pragma unroll
-    for (int p = 0; p < PJ_PARTS; p++) {
+    for (int p = 0; p < PARTS; p++) {
         const float4 v = part[p][x][0][lane], s = part[p][x][1][lane];
         const float f0 = ex2_approx(s.x - b0), f1 = ex2_approx(s.y - b1);
         t.ml.z += s.z * f0, t.ml.w += s.w * f1;
         t.o.x += v.x * f0, t.o.y += v.y * f1, t.o.z += v.z * f0, t.o.w += v.w * f1;
     }
-    const int head = sp.unit / a.head_groups, hg = sp.unit - head * a.head_groups;
+    const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
     const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
-    t.template store<S, QT>(a.out + ((long long)sp.s * a.hq + h0) * D, a.lse ? a.lse + (long long)sp.s * a.hq + h0 : nullptr, heads,
+    t.template store<S, QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
                             E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
 }
 

@@ -2780,10 +2780,18 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
 // The launch of paged_attn. A unit is a sequence's key head with up to 8 or 16
-// of its query heads. While units are few, a cluster of `ways` CTAs takes
-// each, if that leaves its CTAs ATTN_STEPS tiles at most; otherwise the tiles
-// of all units are dealt out evenly, with a join after (split).
-constexpr int ATTN_STEPS = 6, ATTN_WAYS = 16;
+// of its query heads; a cluster of `ways` CTAs takes one, or (split) the tiles
+// of all units are dealt out evenly, with a join after.
+//
+// Measured (us): a step, one tile per CTA, takes 1.05 or what its bytes take
+// at 6.6 TB/s; joining a cluster of 2..8 takes 1.1 and one of 16 takes 4; the
+// split's shares and join take 5. So a cluster is as large as its joining
+// pays for (1000 / 2000 / 4000 tokens, 8 key heads x 128, by 1, 2, 4, 8, 16
+// CTAs and split: 10.4, 8.4, 7.1, 5.5, 7.3, 9.3 / 17.8, 12.2, 9.0, 6.6, 7.3,
+// 10.1 / 33.7, 19.7, 12.9, 8.5, 9.3, 13.4). Only a bound on the lengths is
+// known here and clusters wait for the longest sequence, so past ATTN_STEPS
+// steps the split, which deals out the true lengths, is taken.
+constexpr int ATTN_STEPS = 8;
 
 struct AttnGrid {
     int64_t ctas;
@@ -2794,15 +2802,23 @@ struct AttnGrid {
 static AttnGrid attn_grid(const moss_enc *h, const moss_enc_kv_cache *c, int group, int max_len)
 {
     const int columns = attn_columns(c, group), head_groups = (group + 8 * columns - 1) / (8 * columns);
+    const bool e4m3 = c->dtype == MOSS_ENC_KV_E4M3;
     const int64_t cap = (int64_t)c->page_size * c->pages_per_seq;
     const int64_t bound = max_len > 0 ? std::min<int64_t>(max_len, cap) : cap;
-    const int tile = pa_tile(c->head_dim, c->dtype == MOSS_ENC_KV_E4M3);
+    const int tile = pa_tile(c->head_dim, e4m3);
     const int64_t tiles = (bound + tile - 1) / tile;
     const int64_t units = (int64_t)c->n_seqs * c->n_kv_heads * head_groups;
     const int resident = h->num_sms * (c->head_dim <= 128 && columns == 1 ? 2 : 1);
-    int ways = 1;
-    while (ways < ATTN_WAYS && ways < tiles && units * ways * 2 <= resident) ways *= 2;
-    if (tiles <= (int64_t)ATTN_STEPS * ways && units * ways <= INT32_MAX) return AttnGrid{units * ways, ways, false};
+    int best = 1;
+    double best_us = 1e30;
+    for (int ways = 1; ways <= 16 && ways <= tiles && (ways == 1 || units * ways <= resident); ways *= 2) {
+        const double bytes = 2.0 * tile * c->head_dim * (e4m3 ? 1 : 2) * std::min<double>((double)units * ways, resident);
+        const double waves = std::max(1.0, (double)units * ways / resident);
+        const double us = (double)((tiles + ways - 1) / ways) * waves * std::max(1.05, bytes / 6.6e6) +
+                          (ways == 1 ? 0.0 : ways <= 8 ? 1.1 : 4.0);
+        if (us < best_us) best = ways, best_us = us;
+    }
+    if (tiles <= (int64_t)ATTN_STEPS * best && units * best <= INT32_MAX) return AttnGrid{units * best, best, false};
     return AttnGrid{std::min<int64_t>(units * tiles, resident), 1, true};
 }
 
@@ -2815,7 +2831,7 @@ static int64_t attn_slot_bytes(const moss_enc_kv_cache *c, int group)
 static int64_t attn_workspace(const moss_enc *h, const moss_enc_kv_cache *c, int group, int max_len)
 {
     const AttnGrid g = attn_grid(h, c, group, max_len);
-    return g.split ? g.ctas * (2 * attn_slot_bytes(c, group) + (int64_t)sizeof(PagedSplit)) : 0;
+    return g.split ? g.ctas * 2 * attn_slot_bytes(c, group) : 0;
 }
 
 extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_enc_kv_cache *cache, int n_q_heads, int max_len)
@@ -2855,14 +2871,12 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
     static std::atomic<uint64_t> done{0};
     CUDA_TRY(h, attn_attrs(h, done, paged_attn_kernel<T, QT, E4M3, D, NT>, smem, false));
     float *pieces = static_cast<float *>(workspace);
-    PagedSplit *splits = reinterpret_cast<PagedSplit *>(pieces + (size_t)g.ctas * 2 * S::SLOT);
     {
         Launch L(h, "paged_attn", flops, bytes);
-        CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, pieces, splits));
+        CUDA_TRY(h, launch_k(h, paged_attn_kernel<T, QT, E4M3, D, NT>, grid, block, smem, a, pieces));
     }
     Launch L(h, "paged_join", 0, 0);
-    CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, grid, dim3(2 * D * NT * PJ_PARTS), 0, a, (const float *)pieces,
-                         (const PagedSplit *)splits));
+    CUDA_TRY(h, launch_k(h, paged_join_kernel<T, QT, E4M3, D, NT>, grid, dim3(2 * D * NT * pj_parts(D, NT)), 0, a, (const float *)pieces));
     return MOSS_ENC_OK;
 }
 
