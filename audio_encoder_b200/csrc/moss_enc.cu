@@ -2664,7 +2664,7 @@ static bool row_type_ok(const moss_enc_kv_cache *c, int dtype)
 
 static const char *rows_refusal(const moss_enc_kv_cache *c, const moss_enc_kv_rows *r)
 {
-    if (r->n_rows < 0 || r->n_q_heads < 0 || r->n_q_heads > 65535) return "n_rows or n_q_heads out of range";
+    if (r->n_rows < 0 || r->n_rows > (1 << 30) || r->n_q_heads < 0 || r->n_q_heads > 65535) return "n_rows or n_q_heads out of range";
     if (!row_type_ok(c, r->dtype)) return "rows must be of the cache's 16-bit type (either with an e4m3 cache)";
     if (r->rotary < 0 || r->rotary > c->head_dim || r->rotary % 16 != 0 || (r->rotary > 0 && !r->inv_freq) ||
         !aligned(r->inv_freq, 8) || r->interleaved < 0 || r->interleaved > 1)
@@ -2756,6 +2756,7 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     a.positions = r->positions;
     a.seqs = r->seqs;
     a.inv_freq = r->inv_freq;
+    a.n_rows = r->n_rows;
     a.hq = r->n_q_heads;
     a.rotary = r->rotary;
     a.interleaved = r->interleaved;
@@ -2766,11 +2767,17 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     Launch L(h, "kv_append", 3.0 * r->n_rows * r->rotary * (r->n_q_heads + cache->n_kv_heads),
              (double)r->n_rows * (4.0 * q_row + 2.0 * kv_row * (e4m3 ? 3 : 4) + 8.0));
     const int items = (r->n_q_heads + 2 * cache->n_kv_heads) * (cache->head_dim / 16);
-    const dim3 grid(r->n_rows), block(std::min(256, std::max(64, (items + 31) / 32 * 32)));
-    if (r->dtype == MOSS_ENC_KV_BF16)
-        CUDA_TRY(h, launch_k(h, e4m3 ? kv_append_kernel<bf16, true> : kv_append_kernel<bf16, false>, grid, block, 0, a));
-    else
-        CUDA_TRY(h, launch_k(h, e4m3 ? kv_append_kernel<__half, true> : kv_append_kernel<__half, false>, grid, block, 0, a));
+    const dim3 block(std::min(256, std::max(64, (items + 31) / 32 * 32)));
+    // four rows a CTA once that still gives every SM eight CTAs' worth
+    const int rows = r->n_rows >= 4 * 8 * h->num_sms ? 4 : 1;
+    const dim3 grid((r->n_rows + rows - 1) / rows);
+    const bool b = r->dtype == MOSS_ENC_KV_BF16;
+    void (*kern)(AppendArgs) =
+        rows == 4 ? (b ? (e4m3 ? kv_append_kernel<bf16, true, 4> : kv_append_kernel<bf16, false, 4>)
+                       : (e4m3 ? kv_append_kernel<__half, true, 4> : kv_append_kernel<__half, false, 4>))
+                  : (b ? (e4m3 ? kv_append_kernel<bf16, true, 1> : kv_append_kernel<bf16, false, 1>)
+                       : (e4m3 ? kv_append_kernel<__half, true, 1> : kv_append_kernel<__half, false, 1>));
+    CUDA_TRY(h, launch_k(h, kern, grid, block, 0, a));
     return MOSS_ENC_OK;
 }
 

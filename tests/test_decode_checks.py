@@ -65,7 +65,7 @@ def test_caches_that_are_taken(kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(n_rows=-1), dict(n_q_heads=-1), dict(dtype=binding.KV_F16), dict(dtype=binding.KV_E4M3), dict(rotary=8),
+    dict(n_rows=-1), dict(n_rows=(1 << 30) + 1), dict(n_q_heads=-1), dict(dtype=binding.KV_F16), dict(dtype=binding.KV_E4M3), dict(rotary=8),
     dict(rotary=144), dict(rotary=-16), dict(inv_freq=None), dict(inv_freq=P + 4), dict(interleaved=2),
     dict(k_stride=1028), dict(k_stride=512), dict(q_stride=1024), dict(q_out_stride=2052), dict(k=None), dict(v=None),
     dict(positions=None), dict(q=None), dict(q_out=None), dict(k=P + 8), dict(q_out=P + 4), dict(positions=P + 1),

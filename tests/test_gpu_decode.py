@@ -253,6 +253,10 @@ APPENDS = [
     (2, 17, 16, 8, 1, 256, BF16, BF16, 16, False, "token"),
     (3, 33, 16, 6, 2, 128, BF16, BF16, 0, False, "token"),
     (1, 700, 128, 64, 4, 128, BF16, BF16, 128, False, "token"),
+    # enough rows for several a CTA, an odd number of them
+    (13, 900, 64, 4, 2, 64, F16, F16, 64, True, "token"),
+    (13, 901, 16, 3, 3, 128, BF16, E4M3, 64, False, "head"),
+    (6, 2500, 256, 24, 4, 256, BF16, BF16, 256, False, "token"),
 ]
 
 
