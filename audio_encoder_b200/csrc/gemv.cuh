@@ -22,7 +22,7 @@ namespace moss {
 
 enum : int { GV_BF16 = 0, GV_GELU_BF16 = 1, GV_RESID_F32 = 2, GV_F32 = 5 };  // as moss_enc_gemm's epilogues
 
-static constexpr int GV_WARPS = 8;
+static constexpr int GV_DEPTH = 4;  // groups of codes that a warp has on the way
 
 struct GemvArgs {
     const bf16 *x;         // [M][K]
@@ -31,6 +31,8 @@ struct GemvArgs {
     const float *bias;     // [N] or null
     void *out;             // [M][N]
     int M, N, K, epi;
+    int split;    // warps that share a row tile's groups
+    int k_stage;  // k of x that shared memory holds at a time
 };
 
 // d (fp32 16 x 8) += a (bf16 16 x 16) * b (bf16 16 x 8)
@@ -62,28 +64,80 @@ __device__ __forceinline__ uint4 ldg_stream16(const void *p)
     return v;
 }
 
-// One CTA per 16 rows of N; its warps take the groups of 128 k in turn and
-// add their sums in shared memory.  A lane holds 32 consecutive codes of rows
-// g and g + 8 of a group (one 16-byte load each), k = 32 t .. 32 t + 31; the
-// order of k inside an instruction is free, so its k pairs are (j, j + 4) of
-// each word, the pairs that one mask takes out, and x is paired the same way.
-template <int MT>
-__global__ void __launch_bounds__(32 * GV_WARPS) gemv_q4_kernel(GemvArgs a)
-{
-    __shared__ float red[GV_WARPS][MT * 8][17];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int n0 = blockIdx.x * 16;
-    const int r0 = min(n0 + g, a.N - 1), r1 = min(n0 + g + 8, a.N - 1);
-    const int groups = a.K >> 7;
-    grid_dep_wait();
-    grid_dep_launch();
+__host__ __device__ constexpr size_t gv_red_bytes(int mt, int warps) { return sizeof(float) * 2 * warps * mt * 8 * 17; }
 
-    float acc[MT][4] = {};
-    for (int kg = warp; kg < groups; kg += GV_WARPS) {
-        const uint4 c0 = ldg_stream16(a.codes + (size_t)r0 * (a.K / 2) + kg * 64 + t * 16);
-        const uint4 c1 = ldg_stream16(a.codes + (size_t)r1 * (a.K / 2) + kg * 64 + t * 16);
-        const float s0 = a.scales[(size_t)kg * a.N + r0], s1 = a.scales[(size_t)kg * a.N + r1];
-        const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
+// Persistent CTAs of WARPS warps. A row tile is 16 rows of N; `split` warps
+// share one, taking its groups of 128 k in turn, and add their sums in shared
+// memory; the CTA's WARPS / split row tiles make its tile.
+//
+// A lane holds 32 consecutive codes of rows g and g + 8 of a group (one 16-byte
+// load each), k = 32 t .. 32 t + 31; the order of k inside an instruction is
+// free, so its k pairs are (j, j + 4) of each word, the pairs that one mask
+// takes out, and x is paired the same way when it is put into shared memory,
+// in the order in which the lanes read it. Codes are asked for GV_DEPTH groups
+// ahead, across tiles: 4 KB a warp, 64 KB an SM. (Reading x through the
+// first-level cache instead, in its own order, used up that cache's rate: 8 x
+// 131071 x 2048 took 52.7 us.)
+//
+// The order of the sums depends on N and K alone, so a row of x gives the same
+// bits whatever other rows are with it.
+template <int MT, int WARPS, bool STAGED>
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArgs a)
+{
+    extern __shared__ __align__(16) uint8_t gv_smem[];
+    float(*red)[MT * 8][17] = reinterpret_cast<float(*)[MT * 8][17]>(gv_smem);  // [2 WARPS]
+    uint4 *xs = reinterpret_cast<uint4 *>(gv_smem + gv_red_bytes(MT, WARPS));    // [k / 32][word][M][t]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int split = a.split, wk = warp % split, wn = warp / split, per_cta = WARPS / split;
+    const int groups = a.K >> 7, row_tiles = (a.N + 15) >> 4, cta_tiles = (row_tiles + per_cta - 1) / per_cta;
+    const size_t row_bytes = (size_t)a.K / 2;
+
+    struct Item {
+        uint4 c0, c1;
+        float s0, s1;
+    } item[GV_DEPTH];
+    // Where this lane's codes and scales of a row tile lie (rows past the
+    // last are the last one), and how far its next group is.
+    const uint8_t *c0, *c1;
+    const float *s0, *s1;
+    const size_t c_step = (size_t)split * 64, s_step = (size_t)split * a.N;
+    const auto point = [&](int tile, int kg) {
+        const long long n = (long long)(tile * per_cta + wn) * 16 + g;
+        const long long r0 = min(n, (long long)a.N - 1), r1 = min(n + 8, (long long)a.N - 1);
+        c0 = a.codes + r0 * row_bytes + kg * 64 + t * 16;
+        c1 = a.codes + r1 * row_bytes + kg * 64 + t * 16;
+        s0 = a.scales + (size_t)kg * a.N + r0;
+        s1 = a.scales + (size_t)kg * a.N + r1;
+    };
+    const auto fetch = [&](Item &x) {
+        x.c0 = ldg_stream16(c0);
+        x.c1 = ldg_stream16(c1);
+        x.s0 = *s0;
+        x.s1 = *s1;
+        c0 += c_step, c1 += c_step, s0 += s_step, s1 += s_step;
+    };
+    // x for k of [k0, k0 + n): pairs (x0, x4), (x1, x5), (x2, x6), (x3, x7)
+    const auto stage = [&](int k0, int n) {
+        const int units = a.M * (n >> 3);
+        for (int u = tid; u < units; u += 32 * WARPS) {
+            const int tt = u & 3, m = (u >> 2) % a.M, w = (u >> 2) / a.M;  // w: word within the groups
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + k0 + (w >> 2) * 128 + tt * 32 + (w & 3) * 8);
+            xs[u] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                               __byte_perm(v.y, v.w, 0x7632));
+        }
+    };
+    int col[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; mt++) col[mt] = min(mt * 8 + g, a.M - 1) * 4 + t;
+    float acc[MT][4];
+    const auto clear = [&] {
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.0f;
+    };
+    // a group's products; at: the group's place in xs
+    const auto take = [&](const Item &x, int at) {
+        const uint32_t w0[4] = {x.c0.x, x.c0.y, x.c0.z, x.c0.w}, w1[4] = {x.c1.x, x.c1.y, x.c1.z, x.c1.w};
+        const uint4 *xg = xs + (size_t)at * 16 * a.M;
         float part[MT][4] = {};
 #pragma unroll
         for (int w = 0; w < 4; w++) {
@@ -95,46 +149,109 @@ __global__ void __launch_bounds__(32 * GV_WARPS) gemv_q4_kernel(GemvArgs a)
             }
 #pragma unroll
             for (int mt = 0; mt < MT; mt++) {
-                const int m = mt * 8 + g;
-                uint4 xv = make_uint4(0, 0, 0, 0);
-                if (m < a.M) xv = *reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + kg * 128 + t * 32 + w * 8);
-                // (x0, x1), (x2, x3), (x4, x5), (x6, x7) -> (x0, x4), (x1, x5), (x2, x6), (x3, x7)
-                mma_16816_bf16(part[mt], p0[0], p1[0], p0[1], p1[1], __byte_perm(xv.x, xv.z, 0x5410),
-                               __byte_perm(xv.x, xv.z, 0x7632));
-                mma_16816_bf16(part[mt], p0[2], p1[2], p0[3], p1[3], __byte_perm(xv.y, xv.w, 0x5410),
-                               __byte_perm(xv.y, xv.w, 0x7632));
+                // columns past the last row repeat it; nobody reads their sums
+                const uint4 xv = xg[w * a.M * 4 + col[mt]];
+                mma_16816_bf16(part[mt], p0[0], p1[0], p0[1], p1[1], xv.x, xv.y);
+                mma_16816_bf16(part[mt], p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
             }
         }
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            acc[mt][0] = fmaf(part[mt][0], s0, acc[mt][0]);
-            acc[mt][1] = fmaf(part[mt][1], s0, acc[mt][1]);
-            acc[mt][2] = fmaf(part[mt][2], s1, acc[mt][2]);
-            acc[mt][3] = fmaf(part[mt][3], s1, acc[mt][3]);
+            acc[mt][0] = fmaf(part[mt][0], x.s0, acc[mt][0]);
+            acc[mt][1] = fmaf(part[mt][1], x.s0, acc[mt][1]);
+            acc[mt][2] = fmaf(part[mt][2], x.s1, acc[mt][2]);
+            acc[mt][3] = fmaf(part[mt][3], x.s1, acc[mt][3]);
         }
-    }
+    };
+    // The sums of the row tile's warps and the epilogue; two buffers, so that
+    // one barrier a tile is enough. Warps of a CTA come here once a tile each,
+    // from different places of the unrolled loop.
+    int buf = 0;
+    const auto finish = [&](int tile) {
+        float(*mine)[17] = red[buf * WARPS + warp];
 #pragma unroll
-    for (int mt = 0; mt < MT; mt++) {
-        red[warp][mt * 8 + 2 * t][g] = acc[mt][0];
-        red[warp][mt * 8 + 2 * t + 1][g] = acc[mt][1];
-        red[warp][mt * 8 + 2 * t][g + 8] = acc[mt][2];
-        red[warp][mt * 8 + 2 * t + 1][g + 8] = acc[mt][3];
-    }
-    __syncthreads();
-    for (int i = tid; i < MT * 8 * 16; i += 32 * GV_WARPS) {
-        const int m = i >> 4, r = i & 15, n = n0 + r;
-        if (m >= a.M || n >= a.N) continue;
-        float y = 0.0f;
-#pragma unroll
-        for (int w = 0; w < GV_WARPS; w++) y += red[w][m][r];
-        if (a.bias) y += a.bias[n];
-        const size_t o = (size_t)m * a.N + n;
-        if (a.epi == GV_F32)
-            static_cast<float *>(a.out)[o] = y;
-        else if (a.epi == GV_RESID_F32)
-            static_cast<float *>(a.out)[o] += y;
+        for (int mt = 0; mt < MT; mt++) {
+            mine[mt * 8 + 2 * t][g] = acc[mt][0];
+            mine[mt * 8 + 2 * t + 1][g] = acc[mt][1];
+            mine[mt * 8 + 2 * t][g + 8] = acc[mt][2];
+            mine[mt * 8 + 2 * t + 1][g + 8] = acc[mt][3];
+        }
+        if (split > 1)
+            named_bar_sync(1, 32 * WARPS);
         else
-            static_cast<bf16 *>(a.out)[o] = __float2bfloat16(a.epi == GV_GELU_BF16 ? gelu_fast(y) : y);
+            __syncwarp();
+        for (int i = wk * 32 + lane; i < a.M * 16; i += split * 32) {
+            const int m = i >> 4, r = i & 15;
+            const long long n = (long long)(tile * per_cta + wn) * 16 + r;
+            if (n >= a.N) continue;
+            float y = 0.0f;
+            for (int w = 0; w < split; w++) y += red[buf * WARPS + wn * split + w][m][r];
+            if (a.bias) y += a.bias[n];
+            const size_t o = (size_t)m * a.N + n;
+            if (a.epi == GV_F32)
+                static_cast<float *>(a.out)[o] = y;
+            else if (a.epi == GV_RESID_F32)
+                static_cast<float *>(a.out)[o] += y;
+            else
+                static_cast<bf16 *>(a.out)[o] = __float2bfloat16(a.epi == GV_GELU_BF16 ? gelu_fast(y) : y);
+        }
+        buf ^= 1;
+        clear();
+    };
+    grid_dep_wait();
+    grid_dep_launch();
+    clear();
+    if constexpr (STAGED) {
+        for (int tile = blockIdx.x; tile < cta_tiles; tile += gridDim.x) {
+            for (int k0 = 0; k0 < a.K; k0 += a.k_stage) {
+                const int n = min(a.k_stage, a.K - k0) >> 7;
+                __syncthreads();
+                stage(k0, 128 * n);
+                __syncthreads();
+                point(tile, (k0 >> 7) + wk);
+                for (int kg = wk; kg < n; kg += GV_DEPTH * split) {
+#pragma unroll
+                    for (int d = 0; d < GV_DEPTH; d++)
+                        if (kg + d * split < n) fetch(item[d]);
+#pragma unroll
+                    for (int d = 0; d < GV_DEPTH; d++)
+                        if (kg + d * split < n) take(item[d], kg + d * split);
+                }
+            }
+            finish(tile);
+        }
+    } else {
+        int next_tile = blockIdx.x, next_kg = wk;  // what is asked for next
+        const auto ask = [&](Item &x) {
+            if (next_tile >= cta_tiles) return;
+            fetch(x);
+            next_kg += split;
+            if (next_kg >= groups) {
+                next_kg = wk;
+                next_tile += gridDim.x;
+                point(next_tile, wk);
+            }
+        };
+        point(next_tile, wk);
+#pragma unroll
+        for (int d = 0; d < GV_DEPTH; d++) ask(item[d]);
+        stage(0, a.K);
+        __syncthreads();
+        int tile = blockIdx.x, kg = wk;
+        while (tile < cta_tiles) {
+#pragma unroll
+            for (int d = 0; d < GV_DEPTH; d++) {
+                if (tile >= cta_tiles) break;
+                take(item[d], kg);
+                ask(item[d]);
+                kg += split;
+                if (kg >= groups) {
+                    finish(tile);
+                    kg = wk;
+                    tile += gridDim.x;
+                }
+            }
+        }
     }
 }
 

@@ -2587,6 +2587,61 @@ struct OnDevice {
 
 static bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// A kernel's attributes, once per device (`done`: a bit for each).
+template <class K>
+static cudaError_t kernel_attrs(const moss_enc *h, std::atomic<uint64_t> &done, K *kern, size_t smem, bool clusters)
+{
+    const uint64_t bit = h->device < 64 ? uint64_t(1) << h->device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+// Warps that share a row tile of gemv_q4: as few as fill the SMs' 16 warps each
+// in whole rounds (a round more for each warp that a tile is split over is
+// 3 % of it: the sums' way through shared memory). Of N and K only, so that
+// the order of the sums does not depend on the number of rows.
+static int gemv_split(int sms, int N, int K)
+{
+    const double tiles = (N + 15) / 16, warps = 16.0 * sms;
+    int best = 1;
+    double best_cost = 1e30;
+    for (int split = 1; split <= 8 && split <= K / 128; split *= 2) {
+        const double cost = std::ceil(tiles * split / warps) / split * (1.0 + 0.03 * split);
+        if (cost < best_cost) best = split, best_cost = cost;
+    }
+    return best;
+}
+
+template <int MT, int WARPS, bool STAGED = false>
+static moss_enc_status gemv_launch(moss_enc *h, const GemvArgs &a, size_t smem)
+{
+    static std::atomic<uint64_t> done{0};
+    CUDA_TRY(h, kernel_attrs(h, done, gemv_q4_kernel<MT, WARPS, STAGED>, SMEM_LIMIT, false));
+    const int per_cta = WARPS / a.split;
+    const int64_t tiles = ((int64_t)a.N + 15) / 16;
+    const int64_t ctas = std::min<int64_t>((tiles + per_cta - 1) / per_cta, (int64_t)h->num_sms * (16 / WARPS));
+    CUDA_TRY(h, launch_k(h, gemv_q4_kernel<MT, WARPS, STAGED>, dim3((unsigned)ctas), dim3(32 * WARPS), smem, a));
+    return MOSS_ENC_OK;
+}
+
+// Two CTAs of 8 warps an SM while all of x fits half of its shared memory, one
+// of 16 warps otherwise, which takes x in stages when even that is too little
+// (whole rounds of the warps that share a tile, so no sum changes its order).
+template <int MT>
+static moss_enc_status gemv_run(moss_enc *h, GemvArgs a)
+{
+    const size_t x = (size_t)a.M * a.K * 2;
+    a.k_stage = a.K;
+    if (x + gv_red_bytes(MT, 8) <= SMEM_LIMIT / 2 - 1024) return gemv_launch<MT, 8>(h, a, x + gv_red_bytes(MT, 8));
+    const size_t room = SMEM_LIMIT - gv_red_bytes(MT, 16);
+    if (x <= room) return gemv_launch<MT, 16>(h, a, x + gv_red_bytes(MT, 16));
+    a.k_stage = (int)(room / (256 * (size_t)a.M * a.split)) * 128 * a.split;
+    return gemv_launch<MT, 16, true>(h, a, (size_t)a.M * a.k_stage * 2 + gv_red_bytes(MT, 16));
+}
+
 extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs,
                                             const float *bias, void *out, int M, int N, int K, int epilogue)
 {
@@ -2613,14 +2668,10 @@ extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const vo
     OnDevice dev(h);
     Launch L(h, "gemv_q4", 2.0 * M * N * K, 0.5 * N * (double)K + 4.0 * N * (K / 128) + 2.0 * M * K +
                                                 (epilogue == GV_RESID_F32 ? 8.0 : wide ? 4.0 : 2.0) * M * N);
-    const dim3 grid((N + 15) / 16), block(32 * GV_WARPS);
-    if (M <= 8)
-        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<1>, grid, block, 0, a));
-    else if (M <= 16)
-        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<2>, grid, block, 0, a));
-    else
-        CUDA_TRY(h, launch_k(h, gemv_q4_kernel<4>, grid, block, 0, a));
-    return MOSS_ENC_OK;
+    a.split = gemv_split(h->num_sms, N, K);
+    if (M <= 8) return gemv_run<1>(h, a);
+    if (M <= 16) return gemv_run<2>(h, a);
+    return gemv_run<4>(h, a);
 }
 
 // The reasons for which the paged calls refuse their arguments (null: none);
@@ -2769,7 +2820,7 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     const int items = (r->n_q_heads + 2 * cache->n_kv_heads) * (cache->head_dim / 16);
     const dim3 block(std::min(256, std::max(64, (items + 31) / 32 * 32)));
     // four rows a CTA once that still gives every SM eight CTAs' worth
-    const int rows = r->n_rows >= 4 * 8 * h->num_sms ? 4 : 1;
+    const int rows = r->n_rows >= 4 * h->num_sms ? 4 : 1;
     const dim3 grid((r->n_rows + rows - 1) / rows);
     const bool b = r->dtype == MOSS_ENC_KV_BF16;
     void (*kern)(AppendArgs) =
@@ -2847,18 +2898,6 @@ extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_e
     return attn_workspace(h, cache, n_q_heads / cache->n_kv_heads, max_len);
 }
 
-// A kernel's attributes, once per device (`done`: a bit for each).
-template <class K>
-static cudaError_t attn_attrs(const moss_enc *h, std::atomic<uint64_t> &done, K *kern, size_t smem, bool clusters)
-{
-    const uint64_t bit = h->device < 64 ? uint64_t(1) << h->device : 0;
-    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-    return e;
-}
-
 template <typename T, typename QT, bool E4M3, int D, int NT>
 static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const AttnGrid &g, void *workspace, double flops,
                                       double bytes)
@@ -2870,13 +2909,13 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
     if (!g.split) {
         const auto kern = paged_attn_unit_kernel<T, QT, E4M3, D, NT>;
         static std::atomic<uint64_t> done{0};
-        CUDA_TRY(h, attn_attrs(h, done, kern, smem_ways, true));
+        CUDA_TRY(h, kernel_attrs(h, done, kern, smem_ways, true));
         Launch L(h, "paged_attn", flops, bytes);
         CUDA_TRY(h, launch_cluster(h, kern, g.ways, grid, block, g.ways > 1 ? smem_ways : smem, a, g.ways));
         return MOSS_ENC_OK;
     }
     static std::atomic<uint64_t> done{0};
-    CUDA_TRY(h, attn_attrs(h, done, paged_attn_kernel<T, QT, E4M3, D, NT>, smem, false));
+    CUDA_TRY(h, kernel_attrs(h, done, paged_attn_kernel<T, QT, E4M3, D, NT>, smem, false));
     float *pieces = static_cast<float *>(workspace);
     {
         Launch L(h, "paged_attn", flops, bytes);

@@ -90,7 +90,7 @@ def gelu64(y):
 
 SHAPES = [(1, 1, 128), (1, 17, 128), (3, 31, 384), (8, 1280, 1280), (9, 1281, 1280), (13, 5120, 1280), (16, 1279, 896),
           (17, 250, 2048), (25, 2047, 640), (32, 2048, 1152), (1, 40000, 256), (5, 2048, 8192), (2, 3, 65536),
-          (32, 33, 16384)]
+          (32, 33, 16384), (32, 5000, 4096), (7, 131071, 128), (12, 9999, 2176)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
@@ -133,8 +133,9 @@ def test_gemv_q4_counts_every_code(enc):
         assert torch.equal(got.double().cpu(), want[:, k0:k0 + 32].t())
 
 
-def test_gemv_q4_rows_do_not_depend_on_the_others(enc):
-    x, codes, scales, b = gemv_case(32, 333, 1280, 3)
+@pytest.mark.parametrize("N,K", [(333, 1280), (7000, 512), (70000, 384), (50, 16384), (4100, 2176)])
+def test_gemv_q4_rows_do_not_depend_on_the_others(enc, N, K):
+    x, codes, scales, b = gemv_case(32, N, K, 3)
     alone = {m: enc.gemv_q4(x[:m].contiguous(), codes, scales, b, epilogue=5) for m in (1, 8, 9, 16, 17, 32)}
     for m, y in alone.items():
         assert torch.equal(y, alone[32][:m]), m
