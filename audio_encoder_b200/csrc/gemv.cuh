@@ -4,10 +4,19 @@
 // with groups of 128 consecutive k.  Every code is read once, so the floor is
 // the codes' bytes (N K / 2, plus N K / 32 of scales) at the memory's rate.
 //
-// The codes stay integers: c - 8 is exact in bf16, the products with x and
-// their sums over a group are taken in fp32 by the tensor cores, and the fp32
-// scale multiplies each group's sum once.  Nothing rounds a weight (the
-// 4-bit GEMM rounds q * s to bf16, because its tiles need bf16 operands).
+// The codes go to the tensor cores as they are: masked out of their word, a
+// pair of codes c in the low byte of each half is the bf16 pair c * 2^-133 (or
+// 16 c * 2^-133), because the first two binades of a binary format are linear
+// in its bits. So a pair costs one AND and every second one half a shift, no
+// conversion and no subtraction (adding 128 to make normal numbers, and taking
+// 136 off, cost twice the integer instructions, which bounded the kernel: 45.4
+// us for 8 x 131071 x 2048). x is multiplied by 2^60 (and by 2^-4 where it
+// meets 16 c), which is exact and keeps the products normal in fp32, and a
+// group's sum starts from -8 times the group's sum of x:
+//   sum (c - 8) x = -8 sum x + sum c x.
+// A group's sum is fp32, and its fp32 scale multiplies it once: nothing rounds
+// a weight (the 4-bit GEMM rounds q * s to bf16, because its tiles need bf16
+// operands). An infinity in a row of x makes that row NaN.
 //
 // mma.sync m16n8k16 rather than tcgen05: the weights are A (16 rows of N),
 // the few rows of x are B (8 columns), and the codes go from registers into
@@ -45,14 +54,11 @@ __device__ __forceinline__ void mma_16816_bf16(float (&d)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes j and j + 4 of a word of eight as a bf16 pair: 0x4300 | c is 128 + c
-// exactly (bf16 has 7 mantissa bits), and subtracting 136 is exact.
+// Codes j and j + 4 of a word of eight, times 1 (even j) or 16 (odd j), as the
+// bf16 pair of that multiple of 2^-133.
 __device__ __forceinline__ uint32_t q4_pair(uint32_t word, int j)
 {
-    const uint32_t v = ((word >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), bias);
-    return *reinterpret_cast<const uint32_t *>(&r);
+    return (j < 2 ? word : word >> 8) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
 
 __device__ __forceinline__ uint4 ldg_stream16(const void *p)
@@ -65,6 +71,9 @@ __device__ __forceinline__ uint4 ldg_stream16(const void *p)
 }
 
 __host__ __device__ constexpr size_t gv_red_bytes(int mt, int warps) { return sizeof(float) * 2 * warps * mt * 8 * 17; }
+// Shared memory of k values of M rows of x: themselves, and a sum and a factor
+// per group.
+__host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { return 2 * (size_t)M * k + mt * 64 * (size_t)(k / 128); }
 
 // Persistent CTAs of WARPS warps. A row tile is 16 rows of N; `split` warps
 // share one, taking its groups of 128 k in turn, and add their sums in shared
@@ -86,7 +95,9 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
 {
     extern __shared__ __align__(16) uint8_t gv_smem[];
     float(*red)[MT * 8][17] = reinterpret_cast<float(*)[MT * 8][17]>(gv_smem);  // [2 WARPS]
-    uint4 *xs = reinterpret_cast<uint4 *>(gv_smem + gv_red_bytes(MT, WARPS));    // [k / 32][word][M][t]
+    float *xsum = reinterpret_cast<float *>(gv_smem + gv_red_bytes(MT, WARPS));  // [k / 128][MT * 8]
+    float *xshort = xsum + MT * 8 * (min(a.k_stage, a.K) >> 7);                  // the same
+    uint4 *xs = reinterpret_cast<uint4 *>(xshort + MT * 8 * (min(a.k_stage, a.K) >> 7));  // [k / 128][word][M][t]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = a.split, wk = warp % split, wn = warp / split, per_cta = WARPS / split;
     const int groups = a.K >> 7, row_tiles = (a.N + 15) >> 4, cta_tiles = (row_tiles + per_cta - 1) / per_cta;
@@ -116,15 +127,58 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
         x.s1 = *s1;
         c0 += c_step, c1 += c_step, s0 += s_step, s1 += s_step;
     };
-    // x for k of [k0, k0 + n): pairs (x0, x4), (x1, x5), (x2, x6), (x3, x7)
+    // x for k of [k0, k0 + n), scaled, in pairs (x0, x4), (x1, x5) / 16, (x2,
+    // x6), (x3, x7) / 16, and the groups' sums; a thread has 32 values of a row.
+    // A group with a value of 2^66 or more, which 2^60 times itself might not
+    // hold, is not scaled, and says by which factor its sums fall short.
+    bool huge = false;  // whether any group is such a one
     const auto stage = [&](int k0, int n) {
-        const int units = a.M * (n >> 3);
-        for (int u = tid; u < units; u += 32 * WARPS) {
-            const int tt = u & 3, m = (u >> 2) % a.M, w = (u >> 2) / a.M;  // w: word within the groups
-            const uint4 v = *reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + k0 + (w >> 2) * 128 + tt * 32 + (w & 3) * 8);
-            xs[u] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                               __byte_perm(v.y, v.w, 0x7632));
+        bool mine = false;
+        for (int u = tid; u < (n >> 5) * a.M; u += 32 * WARPS) {
+            const int tt = u & 3, m = (u >> 2) % a.M, kg = (u >> 2) / a.M;
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + k0 + kg * 128 + tt * 32);
+            uint4 in[4];
+#pragma unroll
+            for (int w = 0; w < 4; w++) in[w] = src[w];
+            float sum = 0.0f, top = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                const uint32_t p[4] = {in[w].x, in[w].y, in[w].z, in[w].w};
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&p[j]));
+                    sum += f.x + f.y;
+                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            // a row's four threads are neighbours, and all here
+            const uint32_t four = 0xFu << (lane & 28);
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+                sum += __shfl_xor_sync(four, sum, d);
+                top = fmaxf(top, __shfl_xor_sync(four, top, d));
+            }
+            const bool big = top >= 0x1p66f;
+            mine |= big;
+            const float up = big ? 1.0f : 0x1p60f;
+            const __nv_bfloat162 u1 = __float2bfloat162_rn(up), u16 = __float2bfloat162_rn(up * 0.0625f);
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                uint32_t p[4] = {__byte_perm(in[w].x, in[w].z, 0x5410), __byte_perm(in[w].x, in[w].z, 0x7632),
+                                 __byte_perm(in[w].y, in[w].w, 0x5410), __byte_perm(in[w].y, in[w].w, 0x7632)};
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&p[j]), j & 1 ? u16 : u1);
+                    p[j] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                xs[((kg * 4 + w) * a.M + m) * 4 + tt] = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+            if (tt == 0) {
+                xsum[kg * MT * 8 + m] = sum * (-8.0f * 0x1p-73f) * (up * 0x1p-60f);
+                xshort[kg * MT * 8 + m] = big ? 0x1p60f : 1.0f;
+            }
         }
+        huge = __syncthreads_or(mine);
     };
     int col[MT];
 #pragma unroll
@@ -138,7 +192,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
     const auto take = [&](const Item &x, int at) {
         const uint32_t w0[4] = {x.c0.x, x.c0.y, x.c0.z, x.c0.w}, w1[4] = {x.c1.x, x.c1.y, x.c1.z, x.c1.w};
         const uint4 *xg = xs + (size_t)at * 16 * a.M;
-        float part[MT][4] = {};
+        float part[MT][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; mt++) {
+            const float2 b = *reinterpret_cast<const float2 *>(xsum + (at * MT + mt) * 8 + 2 * t);
+            part[mt][0] = part[mt][2] = b.x, part[mt][1] = part[mt][3] = b.y;
+        }
 #pragma unroll
         for (int w = 0; w < 4; w++) {
             uint32_t p0[4], p1[4];
@@ -155,12 +214,18 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 mma_16816_bf16(part[mt], p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
             }
         }
+        // the sums are 2^(60 - 133) of themselves
+        const float s0 = x.s0 * 0x1p73f, s1 = x.s1 * 0x1p73f;
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
-            acc[mt][0] = fmaf(part[mt][0], x.s0, acc[mt][0]);
-            acc[mt][1] = fmaf(part[mt][1], x.s0, acc[mt][1]);
-            acc[mt][2] = fmaf(part[mt][2], x.s1, acc[mt][2]);
-            acc[mt][3] = fmaf(part[mt][3], x.s1, acc[mt][3]);
+            if (huge) {
+                const float2 f = *reinterpret_cast<const float2 *>(xshort + (at * MT + mt) * 8 + 2 * t);
+                part[mt][0] *= f.x, part[mt][1] *= f.y, part[mt][2] *= f.x, part[mt][3] *= f.y;
+            }
+            acc[mt][0] = fmaf(part[mt][0], s0, acc[mt][0]);
+            acc[mt][1] = fmaf(part[mt][1], s0, acc[mt][1]);
+            acc[mt][2] = fmaf(part[mt][2], s1, acc[mt][2]);
+            acc[mt][3] = fmaf(part[mt][3], s1, acc[mt][3]);
         }
     };
     // The sums of the row tile's warps and the epilogue; two buffers, so that
@@ -207,7 +272,6 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 const int n = min(a.k_stage, a.K - k0) >> 7;
                 __syncthreads();
                 stage(k0, 128 * n);
-                __syncthreads();
                 point(tile, (k0 >> 7) + wk);
                 for (int kg = wk; kg < n; kg += GV_DEPTH * split) {
 #pragma unroll
@@ -236,7 +300,6 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
 #pragma unroll
         for (int d = 0; d < GV_DEPTH; d++) ask(item[d]);
         stage(0, a.K);
-        __syncthreads();
         int tile = blockIdx.x, kg = wk;
         while (tile < cta_tiles) {
 #pragma unroll

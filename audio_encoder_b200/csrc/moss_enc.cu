@@ -2633,13 +2633,14 @@ static moss_enc_status gemv_launch(moss_enc *h, const GemvArgs &a, size_t smem)
 template <int MT>
 static moss_enc_status gemv_run(moss_enc *h, GemvArgs a)
 {
-    const size_t x = (size_t)a.M * a.K * 2;
     a.k_stage = a.K;
+    const size_t x = gv_x_bytes(MT, a.M, a.K);
     if (x + gv_red_bytes(MT, 8) <= SMEM_LIMIT / 2 - 1024) return gemv_launch<MT, 8>(h, a, x + gv_red_bytes(MT, 8));
     const size_t room = SMEM_LIMIT - gv_red_bytes(MT, 16);
     if (x <= room) return gemv_launch<MT, 16>(h, a, x + gv_red_bytes(MT, 16));
-    a.k_stage = (int)(room / (256 * (size_t)a.M * a.split)) * 128 * a.split;
-    return gemv_launch<MT, 16, true>(h, a, (size_t)a.M * a.k_stage * 2 + gv_red_bytes(MT, 16));
+    const int round = 128 * a.split;
+    a.k_stage = (int)(room / gv_x_bytes(MT, a.M, round)) * round;
+    return gemv_launch<MT, 16, true>(h, a, gv_x_bytes(MT, a.M, a.k_stage) + gv_red_bytes(MT, 16));
 }
 
 extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs,

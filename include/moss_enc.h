@@ -415,8 +415,11 @@ moss_enc_status moss_enc_nvf4_quant_weights(const void *w, int n, int k, int par
  *  out, epilogue  as moss_enc_gemm: 0 (bf16), 1 (GELU, bf16), 2 (fp32, out +=),
  *             5 (fp32).
  * Any N >= 1; K % 128 == 0; x and Bq 16-byte aligned, Bs, bias and out aligned
- * to their elements.  The sums are fp32 and the scale multiplies a group's
- * sum, so no weight is rounded (moss_enc_gemm_q4 multiplies bf16(q * s)). */
+ * to their elements.  The sums are fp32 (of code * x and of x apart, so their
+ * error is relative to sum |x| (code + 8) Bs) and the scale multiplies a group's
+ * sum, so no weight is rounded (moss_enc_gemm_q4 multiplies bf16(q * s)).  A row
+ * of x gives the same bits whatever other rows are with it; NaN or an infinity
+ * in it makes that row NaN. */
 #define MOSS_ENC_GEMV_MAX_ROWS 32
 moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs, const float *bias,
                                  void *out, int M, int N, int K, int epilogue);

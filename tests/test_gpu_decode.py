@@ -70,15 +70,16 @@ def gemv_case(M, N, K, seed, bias=True):
 
 def gemv_ref(x, codes, scales, b):
     """The product in 64 bits and the bound on a 32-bit sum's error: a group's
-    127 additions, one multiplication, and the sum over groups (warps and all)
-    and the bias."""
+    sum of (q + 8) x less 8 times its sum of x, 127 additions each and one
+    more, whose partial sums sum (q + 8) |x| + 8 sum |x| bounds; two
+    multiplications, and the sum over groups (warps and all) and the bias."""
     K = x.shape[1]
-    w = unpack(codes) * scales.double().repeat_interleave(128, 0).t()
-    y = x.double() @ w.t()
-    size = x.double().abs() @ w.abs().t()
+    s = scales.double().repeat_interleave(128, 0).t()
+    y = x.double() @ (unpack(codes) * s).t()
+    size = x.double().abs() @ ((unpack(codes) + 16) * s).t()
     if b is not None:
         y, size = y + b.double(), size + b.double().abs()
-    return y, size * U * (128 + 1 + K // 128 + 16)
+    return y, size * U * (128 + 3 + K // 128 + 16)
 
 
 GELU_SLOPE = 1.13  # the largest slope of x Phi(x)
@@ -149,6 +150,25 @@ def test_gemv_q4_passes_on_nan_and_infinity(enc):
     assert torch.isnan(y[1]).all() and not torch.isfinite(y[2]).any()
     ref, tol = gemv_ref(x[[0, 3]], codes, scales, b)
     within(y[[0, 3]], ref, tol)
+
+
+@pytest.mark.parametrize("rows", [1, 8, 32])
+def test_gemv_q4_large_and_small_values(enc, rows):
+    # rows of very different sizes, each to its own precision
+    x, codes, scales, b = gemv_case(rows, 96, 16384 if rows == 32 else 512, 6, bias=False)
+    for top in (1e20, 1e30):
+        size = torch.logspace(-20, math.log10(top), rows).cuda() if rows > 1 else torch.tensor([top]).cuda()
+        xs = (x.float() * size[:, None]).to(BF16)
+        y = enc.gemv_q4(xs, codes, scales, None, epilogue=5)
+        within(y, *gemv_ref(xs, codes, scales, None))
+        assert torch.isfinite(y).all()
+        # and within a row, from group to group
+        xs = (x.float() * torch.logspace(-5, math.log10(top), x.shape[1]).cuda()).to(BF16)
+        within(enc.gemv_q4(xs, codes, scales, None, epilogue=5), *gemv_ref(xs, codes, scales, None))
+    xs = (x.float() * 1e-25).to(BF16)
+    ref, tol = gemv_ref(xs, codes, scales, None)
+    # sums below 2^-126 of what is held, 2^-73 of themselves: 2^-149 steps
+    within(enc.gemv_q4(xs, codes, scales, None, epilogue=5), ref, tol + 2.0 ** (-149 + 73) * x.shape[1] * scales.double().amax())
 
 
 def test_gemv_q4_no_rows_and_refusals(enc):
