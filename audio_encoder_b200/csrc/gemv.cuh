@@ -10,7 +10,7 @@
 // in its bits. So a pair costs one AND and every second one half a shift, no
 // conversion and no subtraction (adding 128 to make normal numbers, and taking
 // 136 off, cost twice the integer instructions, which bounded the kernel: 45.4
-// us for 8 x 131071 x 2048). x is multiplied by 2^60 (and by 2^-4 where it
+// us for 8 x 131071 x 2048). x is multiplied by 2^90 (and by 2^-4 where it
 // meets 16 c), which is exact and keeps the products normal in fp32, and a
 // group's sum starts from -8 times the group's sum of x:
 //   sum (c - 8) x = -8 sum x + sum c x.
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
     };
     // x for k of [k0, k0 + n), scaled, in pairs (x0, x4), (x1, x5) / 16, (x2,
     // x6), (x3, x7) / 16, and the groups' sums; a thread has 32 values of a row.
-    // A group with a value of 2^66 or more, which 2^60 times itself might not
+    // A group with a value of 2^36 or more, which 2^90 times itself might not
     // hold, is not scaled, and says by which factor its sums fall short.
     bool huge = false;  // whether any group is such a one
     const auto stage = [&](int k0, int n) {
@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 sum += __shfl_xor_sync(four, sum, d);
                 top = fmaxf(top, __shfl_xor_sync(four, top, d));
             }
-            const bool big = top >= 0x1p66f;
+            const bool big = top >= 0x1p36f;
             mine |= big;
-            const float up = big ? 1.0f : 0x1p60f;
+            const float up = big ? 1.0f : 0x1p90f;
             const __nv_bfloat162 u1 = __float2bfloat162_rn(up), u16 = __float2bfloat162_rn(up * 0.0625f);
 #pragma unroll
             for (int w = 0; w < 4; w++) {
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 xs[((kg * 4 + w) * a.M + m) * 4 + tt] = make_uint4(p[0], p[1], p[2], p[3]);
             }
             if (tt == 0) {
-                xsum[kg * MT * 8 + m] = sum * (-8.0f * 0x1p-73f) * (up * 0x1p-60f);
-                xshort[kg * MT * 8 + m] = big ? 0x1p60f : 1.0f;
+                xsum[kg * MT * 8 + m] = sum * (-8.0f * 0x1p-43f) * (up * 0x1p-90f);
+                xshort[kg * MT * 8 + m] = big ? 0x1p90f : 1.0f;
             }
         }
         huge = __syncthreads_or(mine);
@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.0f;
     };
-    // a group's products; at: the group's place in xs
+    // a group's products; at: the group's place in xs. The sums stay 2^(90 -
+    // 133) of themselves until the end.
     const auto take = [&](const Item &x, int at) {
         const uint32_t w0[4] = {x.c0.x, x.c0.y, x.c0.z, x.c0.w}, w1[4] = {x.c1.x, x.c1.y, x.c1.z, x.c1.w};
         const uint4 *xg = xs + (size_t)at * 16 * a.M;
@@ -214,23 +215,27 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 mma_16816_bf16(part[mt], p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
             }
         }
-        // the sums are 2^(60 - 133) of themselves
-        const float s0 = x.s0 * 0x1p73f, s1 = x.s1 * 0x1p73f;
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             if (huge) {
                 const float2 f = *reinterpret_cast<const float2 *>(xshort + (at * MT + mt) * 8 + 2 * t);
                 part[mt][0] *= f.x, part[mt][1] *= f.y, part[mt][2] *= f.x, part[mt][3] *= f.y;
             }
-            acc[mt][0] = fmaf(part[mt][0], s0, acc[mt][0]);
-            acc[mt][1] = fmaf(part[mt][1], s0, acc[mt][1]);
-            acc[mt][2] = fmaf(part[mt][2], s1, acc[mt][2]);
-            acc[mt][3] = fmaf(part[mt][3], s1, acc[mt][3]);
+            acc[mt][0] = fmaf(part[mt][0], x.s0, acc[mt][0]);
+            acc[mt][1] = fmaf(part[mt][1], x.s0, acc[mt][1]);
+            acc[mt][2] = fmaf(part[mt][2], x.s1, acc[mt][2]);
+            acc[mt][3] = fmaf(part[mt][3], x.s1, acc[mt][3]);
         }
     };
-    // The sums of the row tile's warps and the epilogue; two buffers, so that
-    // one barrier a tile is enough. Warps of a CTA come here once a tile each,
-    // from different places of the unrolled loop.
+    // The bias of this lane's column of the outputs (all its outputs of a tile
+    // have the same), asked for when the tile begins.
+    float bias = 0.0f;
+    const auto begin = [&](int tile) {
+        const long long n = (long long)(tile * per_cta + wn) * 16 + (lane & 15);
+        if (a.bias && tile < cta_tiles && n < a.N) bias = a.bias[n];
+    };
+    // The sums of the row tile's warps, who wait for one another alone, and the
+    // epilogue. With two buffers one barrier a tile is enough.
     int buf = 0;
     const auto finish = [&](int tile) {
         float(*mine)[17] = red[buf * WARPS + warp];
@@ -242,30 +247,32 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
             mine[mt * 8 + 2 * t + 1][g + 8] = acc[mt][3];
         }
         if (split > 1)
-            named_bar_sync(1, 32 * WARPS);
+            named_bar_sync(1 + wn, 32 * split);
         else
             __syncwarp();
-        for (int i = wk * 32 + lane; i < a.M * 16; i += split * 32) {
-            const int m = i >> 4, r = i & 15;
-            const long long n = (long long)(tile * per_cta + wn) * 16 + r;
-            if (n >= a.N) continue;
-            float y = 0.0f;
-            for (int w = 0; w < split; w++) y += red[buf * WARPS + wn * split + w][m][r];
-            if (a.bias) y += a.bias[n];
-            const size_t o = (size_t)m * a.N + n;
-            if (a.epi == GV_F32)
-                static_cast<float *>(a.out)[o] = y;
-            else if (a.epi == GV_RESID_F32)
-                static_cast<float *>(a.out)[o] += y;
-            else
-                static_cast<bf16 *>(a.out)[o] = __float2bfloat16(a.epi == GV_GELU_BF16 ? gelu_fast(y) : y);
-        }
+        const int r = lane & 15;
+        const long long n = (long long)(tile * per_cta + wn) * 16 + r;
+        if (n < a.N)
+            for (int m = wk * 2 + (lane >> 4); m < a.M; m += split * 2) {
+                float y = 0.0f;
+                for (int w = 0; w < split; w++) y += red[buf * WARPS + wn * split + w][m][r];
+                y = y * 0x1p43f + bias;
+                const size_t o = (size_t)m * a.N + n;
+                if (a.epi == GV_F32)
+                    static_cast<float *>(a.out)[o] = y;
+                else if (a.epi == GV_RESID_F32)
+                    static_cast<float *>(a.out)[o] += y;
+                else
+                    static_cast<bf16 *>(a.out)[o] = __float2bfloat16(a.epi == GV_GELU_BF16 ? gelu_fast(y) : y);
+            }
         buf ^= 1;
         clear();
+        begin(tile + gridDim.x);
     };
     grid_dep_wait();
     grid_dep_launch();
     clear();
+    begin(blockIdx.x);
     if constexpr (STAGED) {
         for (int tile = blockIdx.x; tile < cta_tiles; tile += gridDim.x) {
             for (int k0 = 0; k0 < a.K; k0 += a.k_stage) {
@@ -286,13 +293,14 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
         }
     } else {
         int next_tile = blockIdx.x, next_kg = wk;  // what is asked for next
+        // Not under a condition (past the last tile it is asked for again): the
+        // registers of a conditional load are waited for where the cases meet.
         const auto ask = [&](Item &x) {
-            if (next_tile >= cta_tiles) return;
             fetch(x);
             next_kg += split;
             if (next_kg >= groups) {
                 next_kg = wk;
-                next_tile += gridDim.x;
+                next_tile = min(next_tile + (int)gridDim.x, cta_tiles - 1);
                 point(next_tile, wk);
             }
         };
