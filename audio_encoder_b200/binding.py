@@ -1,7 +1,7 @@
 """Thin ctypes binding of the moss_enc C ABI (``include/moss_enc.h``).
 
-Argument marshalling only: every step of the encoder runs in the CUDA
-library.  PyTorch provides device memory and the stream.  Loading fails
+Argument marshalling only (native, in ``csrc/pycalls.cpp``, for the calls of
+one decoding step): every step of the encoder runs in the CUDA library.  PyTorch provides device memory and the stream.  Loading fails
 loudly if ``libmoss_enc.so`` has not been built; there is no fallback.
 """
 from __future__ import annotations
@@ -13,6 +13,7 @@ import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoss_enc.so")
+PYCALLS_PATH = os.path.join(HERE, "_pycalls.so")
 
 OK = 0
 STATUS = {0: "ok", 1: "invalid argument", 2: "capacity", 3: "out of memory", 4: "cuda error",
@@ -177,6 +178,28 @@ def lib():
     return _lib
 
 
+_pycalls = None
+
+
+def pycalls():
+    """The native side of the single-token calls (raises if it is missing)."""
+    global _pycalls
+    if _pycalls is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries first)
+        if not os.path.exists(PYCALLS_PATH):
+            raise ImportError(f"{PYCALLS_PATH} is not built; run `python -m audio_encoder_b200.build`")
+        spec = importlib.util.spec_from_file_location("audio_encoder_b200._pycalls", PYCALLS_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (L.moss_enc_gemv_q4, L.moss_enc_kv_append,
+                                                                  L.moss_enc_paged_attn, L.moss_enc_paged_attn_workspace)))
+        _pycalls = m
+    return _pycalls
+
+
 def weight_count(n_layers: int) -> int:
     return int(lib().moss_enc_weight_count(n_layers))
 
@@ -249,14 +272,12 @@ class KVCache:
         if page_table.shape[1] > 1 and page_table.stride(1) != 1:
             raise ValueError("a row of page_table must be contiguous")
         self.k, self.v, self.page_table = k, v, page_table
-        self.device, self.dtype, self.types = k.device, k.dtype, types
+        self.device, self.dtype = k.device, k.dtype
         self.n_seqs, self.n_kv_heads, self.head_dim = page_table.shape[0], heads, dim
-        self.rows_dtypes = (torch.bfloat16, torch.float16) if types[k.dtype] == KV_E4M3 else (k.dtype,)
         self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), page_table.data_ptr(), table_stride, strides[0], strides[1],
                                 strides[2], page_table.shape[0], page_table.shape[1], n_pages, page, heads, dim,
                                 types[k.dtype], float(k_scale), float(v_scale))
-        self.ref = ctypes.byref(self.desc)
-        self.workspace = (None, 0)  # of the last (query heads, bound on the lengths) asked for: its bytes
+        self.ref, self.address = ctypes.byref(self.desc), ctypes.addressof(self.desc)
 
 
 class Encoder:
@@ -290,12 +311,13 @@ class Encoder:
         if st != OK:
             raise MossEncError(st, "create failed")
         self.h = h
+        self.hid, self.sid = h.value, stream.cuda_stream
         self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if getattr(self, "h", None):
             lib().moss_enc_destroy(self.h)
-            self.h = None
+            self.h, self.hid = None, 0
 
     def __del__(self):
         try:
@@ -311,6 +333,7 @@ class Encoder:
     def set_stream(self, stream):
         self.stream = stream
         self._check(lib().moss_enc_set_stream(self.h, ctypes.c_void_p(stream.cuda_stream)))
+        self.sid = stream.cuda_stream
 
     def synchronize(self):
         self._check(lib().moss_enc_synchronize(self.h))
@@ -374,60 +397,17 @@ class Encoder:
             raise ValueError("x [M][1280] fp32, codes [M][640], sfa ceil(M/128)*20*512 bytes, g [M]")
         self._check(lib().moss_enc_nvf4_quant_rows(self.h, _ptr(x), _ptr(codes), _ptr(sfa), _ptr(g), M))
 
-    def _on_stream(self, shape, dtype, device):
-        """A new tensor whose memory belongs to the handle's stream."""
-        torch = self.torch
-        if torch.cuda.current_stream(device) == self.stream:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+    def _done(self, r):
+        if type(r) is int:  # a status
+            self._check(r)
+        return r
 
     def gemv_q4(self, x, Bq, Bs, bias=None, out=None, epilogue: int = 0):
-        """out = epi(x @ B.T + bias) for 1..32 rows x [M][K] bf16 and B as 4-bit
+        """out = epi(x @ B.T + bias) for 0..32 rows x [M][K] bf16 and B as 4-bit
         codes Bq [N][K/2] (uint8, even k in the low nibble, code q + 8) with
         group scales Bs [K/128][N] fp32; bias [N] fp32 or None.  Epilogues 0
         (bf16), 1 (GELU, bf16), 2 (fp32, out +=: give out) and 5 (fp32)."""
-        torch = self.torch
-        if x.dim() != 2 or Bq.dim() != 2 or Bs.dim() != 2:
-            raise ValueError("x [M][K], Bq [N][K/2], Bs [K/128][N]")
-        M, K = x.shape
-        N = Bq.shape[0]
-        dt = torch.bfloat16 if epilogue in (0, 1) else torch.float32
-        if (x.dtype != torch.bfloat16 or Bq.dtype != torch.uint8 or Bs.dtype != torch.float32 or Bq.shape[1] * 2 != K
-                or K % 128 or tuple(Bs.shape) != (K // 128, N)
-                or not (x.is_contiguous() and Bq.is_contiguous() and Bs.is_contiguous())):
-            raise ValueError("x [M][K] bf16, Bq [N][K/2] uint8, Bs [K/128][N] fp32, contiguous, K a multiple of 128")
-        if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or not bias.is_contiguous()
-                                 or bias.device != x.device):
-            raise ValueError("bias [N] fp32")
-        if out is None:
-            if epilogue == 2:
-                raise ValueError("epilogue 2 adds to out")
-            out = self._on_stream((M, N), dt, x.device)
-        elif out.dtype != dt or tuple(out.shape) != (M, N) or not out.is_contiguous() or out.device != x.device:
-            raise ValueError("out [M][N], contiguous, bf16 (epilogues 0, 1) or fp32 (2, 5)")
-        if not x.is_cuda or Bq.device != x.device or Bs.device != x.device:
-            raise ValueError("x, Bq, Bs, bias and out must be on the handle's CUDA device")
-        self._device(x.device)
-        self._check(lib().moss_enc_gemv_q4(self.h, x.data_ptr(), Bq.data_ptr(), Bs.data_ptr(),
-                                           None if bias is None else bias.data_ptr(), out.data_ptr(), M, N, K,
-                                           int(epilogue)))
-        return out
-
-    def _device(self, device):
-        if device != self.device:
-            raise ValueError(f"the handle is on {self.device}, the tensors on {device}")
-
-    @staticmethod
-    def _heads(x, rows, heads, dim, dtypes, what):
-        """Row stride of x [rows][heads][dim] whose rows are whole."""
-        if x.dtype not in dtypes or x.dim() != 3 or x.shape[0] != rows or x.shape[2] != dim or \
-                (heads is not None and x.shape[1] != heads):
-            raise ValueError(f"{what}: [rows][heads][head_dim] of the cache's type (bf16 or f16 with an e4m3 cache)")
-        s = x.stride()
-        if s[2] != 1 or (x.shape[1] > 1 and s[1] != dim):
-            raise ValueError(f"{what}: the heads of a row must lie next to one another")
-        return s[0] if rows > 1 else x.shape[1] * dim
+        return self._done(pycalls().gemv_q4(self.hid, self.sid, self.device.index, x, Bq, Bs, bias, out, epilogue))
 
     def kv_append(self, cache, k, v, positions, seqs=None, q=None, q_out=None, inv_freq=None, interleaved=False):
         """Append rows to a KVCache: k, v [rows][n_kv_heads][head_dim], row r
@@ -437,43 +417,8 @@ class Encoder:
         inv_freq, in pairs (i, i + r/2) or, interleaved, (2i, 2i + 1).  q
         [rows][heads][head_dim] is turned into q_out (made here when None; may
         be q).  Returns q_out."""
-        torch = self.torch
-        rows, dim = k.shape[0], cache.head_dim
-        types = cache.rows_dtypes if k.dtype in cache.rows_dtypes else ()
-        dt = (k.dtype,) if types else ()
-        ks = self._heads(k, rows, cache.n_kv_heads, dim, dt, "k")
-        vs = self._heads(v, rows, cache.n_kv_heads, dim, dt, "v")
-        dev = cache.device
-        qs = qos = hq = 0
-        if q is not None:
-            qs = self._heads(q, rows, None, dim, dt, "q")
-            hq = q.shape[1]
-            if q_out is None:
-                q_out = self._on_stream((rows, hq, dim), q.dtype, dev)
-            qos = self._heads(q_out, rows, hq, dim, dt, "q_out")
-            if q.device != dev or q_out.device != dev:
-                raise ValueError("q and q_out must be on the cache's device")
-        elif q_out is not None:
-            raise ValueError("q_out needs q")
-        rotary = 0
-        if inv_freq is not None:
-            if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous() or inv_freq.device != dev:
-                raise ValueError("inv_freq: fp64 [r / 2], contiguous")
-            rotary = 2 * inv_freq.shape[0]
-        if positions.dtype != torch.int32 or positions.shape != (rows,) or not positions.is_contiguous():
-            raise ValueError("positions: int32 [rows]")
-        if seqs is not None and (seqs.dtype != torch.int32 or seqs.shape != (rows,) or not seqs.is_contiguous()
-                                 or seqs.device != dev):
-            raise ValueError("seqs: int32 [rows]")
-        if k.device != dev or v.device != dev or positions.device != dev:
-            raise ValueError("k, v and positions must be on the cache's device")
-        self._device(dev)
-        r = KVRows(k.data_ptr(), v.data_ptr(), q.data_ptr() if hq else None, q_out.data_ptr() if hq else None, ks, vs,
-                   qs, qos, positions.data_ptr(), None if seqs is None else seqs.data_ptr(),
-                   inv_freq.data_ptr() if rotary else None, rows, hq, cache.types[k.dtype], rotary,
-                   1 if interleaved else 0)
-        self._check(lib().moss_enc_kv_append(self.h, cache.ref, ctypes.byref(r)))
-        return q_out
+        return self._done(pycalls().kv_append(self.hid, self.sid, self.device.index, cache.address, k, v, positions, seqs,
+                                              q, q_out, inv_freq, interleaved))
 
     def paged_attn(self, cache, q, lengths, scale=None, out=None, lse=None, return_lse=False, max_len: int = 0,
                    workspace=None):
@@ -483,45 +428,15 @@ class Encoder:
         lengths (0: what the page table holds).  Returns out [n_seqs][heads]
         [head_dim], and the fp32 log-sum-exp [n_seqs][heads] with return_lse.
         workspace: uint8, paged_attn_workspace() bytes (made here when None)."""
-        torch = self.torch
-        dev, dim, n = cache.device, cache.head_dim, cache.n_seqs
-        dt = (q.dtype,) if q.dtype in cache.rows_dtypes else ()
-        qs = self._heads(q, n, None, dim, dt, "q")
-        hq = q.shape[1]
-        if out is None:
-            out = self._on_stream((n, hq, dim), q.dtype, dev)
-        elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous() or out.device != dev:
-            raise ValueError("out: contiguous, of q's shape and type")
-        if lse is None:
-            if return_lse:
-                lse = self._on_stream((n, hq), torch.float32, dev)
-        elif lse.dtype != torch.float32 or lse.shape != (n, hq) or not lse.is_contiguous() or lse.device != dev:
-            raise ValueError("lse: fp32 [n_seqs][heads]")
-        if lengths.dtype != torch.int32 or lengths.shape != (n,) or not lengths.is_contiguous() or lengths.device != dev \
-                or q.device != dev:
-            raise ValueError("lengths: int32 [n_seqs], on the cache's device")
-        self._device(dev)
-        need = self.paged_attn_workspace(cache, hq, max_len)
-        if workspace is None:
-            if need:
-                workspace = self._on_stream((need,), torch.uint8, dev)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
-            raise ValueError("workspace: uint8, contiguous, on the cache's device")
-        a = Attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), lengths.data_ptr(), qs, hq,
-                 cache.types[q.dtype], dim ** -0.5 if scale is None else scale, int(max_len),
-                 None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
-        self._check(lib().moss_enc_paged_attn(self.h, cache.ref, ctypes.byref(a)))
-        return (out, lse) if return_lse else out
+        return self._done(pycalls().paged_attn(self.hid, self.sid, self.device.index, cache.address, q, lengths, scale, out,
+                                               lse, return_lse, max_len, workspace))
 
     def paged_attn_workspace(self, cache, heads: int, max_len: int = 0) -> int:
         """Bytes that paged_attn needs as workspace."""
-        key = (heads, max_len)
-        if cache.workspace[0] != key:
-            need = int(lib().moss_enc_paged_attn_workspace(self.h, cache.ref, heads, int(max_len)))
-            if need < 0:
-                raise MossEncError(1, "paged_attn: cache, heads or max_len refused")
-            cache.workspace = (key, need)
-        return cache.workspace[1]
+        need = int(lib().moss_enc_paged_attn_workspace(self.h, cache.ref, heads, int(max_len)))
+        if need < 0:
+            raise MossEncError(1, "paged_attn: cache, heads or max_len refused")
+        return need
 
     def selftest_timeout(self, limit_ms: int = 50):
         self._check(lib().moss_enc_selftest_timeout(self.h, int(limit_ms)))
