@@ -134,23 +134,27 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
     bool huge = false;  // whether any group is such a one
     const auto stage = [&](int k0, int n) {
         bool mine = false;
-        for (int u = tid; u < (n >> 5) * a.M; u += 32 * WARPS) {
-            const int tt = u & 3, m = (u >> 2) % a.M, kg = (u >> 2) / a.M;
+        // four neighbours have a row's group; a round is 8 WARPS of them
+        const int tt = tid & 3, m_step = 8 * WARPS % a.M, kg_step = 8 * WARPS / a.M;
+        for (int m = (tid >> 2) % a.M, kg = (tid >> 2) / a.M; kg < n >> 7;) {
             const uint4 *src = reinterpret_cast<const uint4 *>(a.x + (size_t)m * a.K + k0 + kg * 128 + tt * 32);
             uint4 in[4];
 #pragma unroll
             for (int w = 0; w < 4; w++) in[w] = src[w];
-            float sum = 0.0f, top = 0.0f;
+            float sum = 0.0f;
+            __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
 #pragma unroll
             for (int w = 0; w < 4; w++) {
                 const uint32_t p[4] = {in[w].x, in[w].y, in[w].z, in[w].w};
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&p[j]));
+                    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&p[j]);
+                    const float2 f = __bfloat1622float2(v);
                     sum += f.x + f.y;
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    most = __hmax2(most, __habs2(v));
                 }
             }
+            float top = fmaxf(__low2float(most), __high2float(most));
             // a row's four threads are neighbours, and all here
             const uint32_t four = 0xFu << (lane & 28);
 #pragma unroll
@@ -177,6 +181,8 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 xsum[kg * MT * 8 + m] = sum * (-8.0f * 0x1p-43f) * (up * 0x1p-90f);
                 xshort[kg * MT * 8 + m] = big ? 0x1p90f : 1.0f;
             }
+            m += m_step, kg += kg_step;
+            if (m >= a.M) m -= a.M, kg++;
         }
         huge = __syncthreads_or(mine);
     };

@@ -2570,16 +2570,22 @@ extern "C" moss_enc_status moss_enc_nvf4_quant_rows(moss_enc *h, const float *x,
 // ------------------------------------------------------- one decoding step
 
 namespace {
-// Makes the handle's device current for a launch and puts the caller's back.
-struct OnDevice {
+// Around a call's launches: the handle's device is current (and the caller's
+// again after it). These kernels wait for earlier ones before they read
+// anything that those may write, so they may start early; the kernel after
+// them may be a GEMM that requests a B operand before it waits, so it may not.
+struct DecodeCall {
+    moss_enc *h;
     int before = -1;
-    explicit OnDevice(const moss_enc *h)
+    explicit DecodeCall(moss_enc *h_) : h(h_)
     {
         int d = -1;
         if (cudaGetDevice(&d) == cudaSuccess && d != h->device && cudaSetDevice(h->device) == cudaSuccess) before = d;
+        h->pdl_skip_once = false;
     }
-    ~OnDevice()
+    ~DecodeCall()
     {
+        h->pdl_skip_once = true;
         if (before >= 0) cudaSetDevice(before);
     }
 };
@@ -2647,8 +2653,8 @@ extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const vo
                                             const float *bias, void *out, int M, int N, int K, int epilogue)
 {
     if (!h) return MOSS_ENC_ERR_INVALID_ARG;
-    if (M < 0 || M > MOSS_ENC_GEMV_MAX_ROWS || N <= 0 || K <= 0 || K % 128 != 0)
-        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "rows must be 0..32, N >= 1 and K a multiple of 128");
+    if (M < 0 || M > MOSS_ENC_GEMV_MAX_ROWS || N <= 0 || K <= 0 || K % 128 != 0 || N > (1 << 30) || K > (1 << 30))
+        return fail(h, MOSS_ENC_ERR_INVALID_ARG, "rows must be 0..32, N >= 1 and K a multiple of 128, both 2^30 at most");
     if (epilogue != GV_BF16 && epilogue != GV_GELU_BF16 && epilogue != GV_RESID_F32 && epilogue != GV_F32)
         return fail(h, MOSS_ENC_ERR_INVALID_ARG, "unsupported epilogue");
     if (M == 0) return MOSS_ENC_OK;
@@ -2666,7 +2672,7 @@ extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const vo
     a.N = N;
     a.K = K;
     a.epi = epilogue;
-    OnDevice dev(h);
+    DecodeCall call(h);
     Launch L(h, "gemv_q4", 2.0 * M * N * K, 0.5 * N * (double)K + 4.0 * N * (K / 128) + 2.0 * M * K +
                                                 (epilogue == GV_RESID_F32 ? 8.0 : wide ? 4.0 : 2.0) * M * N);
     a.split = gemv_split(h->num_sms, N, K);
@@ -2815,7 +2821,7 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     const bool e4m3 = cache->dtype == MOSS_ENC_KV_E4M3;
     a.inv_k_scale = e4m3 ? 1.0f / cache->k_scale : 1.0f;
     a.inv_v_scale = e4m3 ? 1.0f / cache->v_scale : 1.0f;
-    OnDevice dev(h);
+    DecodeCall call(h);
     Launch L(h, "kv_append", 3.0 * r->n_rows * r->rotary * (r->n_q_heads + cache->n_kv_heads),
              (double)r->n_rows * (4.0 * q_row + 2.0 * kv_row * (e4m3 ? 3 : 4) + 8.0));
     const int items = (r->n_q_heads + 2 * cache->n_kv_heads) * (cache->head_dim / 16);
@@ -2968,7 +2974,7 @@ extern "C" moss_enc_status moss_enc_paged_attn(moss_enc *h, const moss_enc_kv_ca
     const double flops = 4.0 * tokens * q_row;
     const double bytes = 2.0 * tokens * cache->n_kv_heads * cache->head_dim * (cache->dtype == MOSS_ENC_KV_E4M3 ? 1 : 2) +
                          4.0 * cache->n_seqs * q_row;
-    OnDevice dev(h);
+    DecodeCall call(h);
     void *ws = p->workspace;
     if (cache->dtype == MOSS_ENC_KV_BF16) return paged_attn_dim<bf16, bf16, false>(h, a, columns, g, ws, flops, bytes);
     if (cache->dtype == MOSS_ENC_KV_F16) return paged_attn_dim<__half, __half, false>(h, a, columns, g, ws, flops, bytes);

@@ -117,3 +117,23 @@ def test_binding_refuses_tensors_that_are_no_cache():
                 (k, k, t)]:  # the last: right, but not on a GPU
         with pytest.raises(ValueError):
             binding.KVCache(*bad)
+
+
+def test_native_marshalling_refuses_what_is_not_on_the_gpu():
+    m = binding.pycalls()  # loads without a GPU
+    x = torch.zeros(1, 128, dtype=torch.bfloat16)
+    codes, scales = torch.zeros(16, 64, dtype=torch.uint8), torch.zeros(1, 16)
+    for bad in [(x, codes, scales), (None, codes, scales), (1, codes, scales)]:
+        with pytest.raises(ValueError):
+            m.gemv_q4(0, 0, 0, *bad, None, None, 0)
+    with pytest.raises(ValueError):
+        m.gemv_q4(0, 0, 0)
+    c = cache()
+    k = torch.zeros(1, 8, 128, dtype=torch.bfloat16)
+    i = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        m.kv_append(0, 0, 0, ctypes.addressof(c), k, k, i, None, None, None, None, False)
+    with pytest.raises(ValueError):
+        m.paged_attn(0, 0, 0, ctypes.addressof(c), k, i, None, None, None, False, 0, None)
+    with pytest.raises(TypeError):
+        m.gemv_q4("handle", 0, 0, x, codes, scales, None, None, 0)
