@@ -31,7 +31,8 @@ namespace moss {
 
 enum : int { GV_BF16 = 0, GV_GELU_BF16 = 1, GV_RESID_F32 = 2, GV_F32 = 5 };  // as moss_enc_gemm's epilogues
 
-static constexpr int GV_DEPTH = 4;  // groups of codes that a warp has on the way
+// Groups of codes that a warp has on the way: 4 KB of 16 or 32 rows.
+__host__ __device__ constexpr int gv_depth(int rt) { return 4 / rt; }
 
 struct GemvArgs {
     const bf16 *x;         // [M][K]
@@ -70,7 +71,11 @@ __device__ __forceinline__ uint4 ldg_stream16(const void *p)
     return v;
 }
 
-__host__ __device__ constexpr size_t gv_red_bytes(int mt, int warps) { return sizeof(float) * 2 * warps * mt * 8 * 17; }
+// The warps' sums, in two buffers.
+__host__ __device__ constexpr size_t gv_red_bytes(int mt, int rt, int warps)
+{
+    return sizeof(float) * 2 * warps * mt * 8 * (16 * rt + 1);
+}
 // Shared memory of k values of M rows of x: themselves, and a sum and a factor
 // per group.
 __host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { return 2 * (size_t)M * k + mt * 64 * (size_t)(k / 128); }
@@ -83,49 +88,52 @@ __host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { re
 // load each), k = 32 t .. 32 t + 31; the order of k inside an instruction is
 // free, so its k pairs are (j, j + 4) of each word, the pairs that one mask
 // takes out, and x is paired the same way when it is put into shared memory,
-// in the order in which the lanes read it. Codes are asked for GV_DEPTH groups
+// in the order in which the lanes read it. Codes are asked for DEPTH groups
 // ahead, across tiles: 4 KB a warp, 64 KB an SM. (Reading x through the
 // first-level cache instead, in its own order, used up that cache's rate: 8 x
 // 131071 x 2048 took 52.7 us.)
 //
 // The order of the sums depends on N and K alone, so a row of x gives the same
 // bits whatever other rows are with it.
-template <int MT, int WARPS, bool STAGED>
+template <int MT, int RT, int WARPS, bool STAGED>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArgs a)
 {
+    constexpr int ROWS = 16 * RT, DEPTH = gv_depth(RT);
     extern __shared__ __align__(16) uint8_t gv_smem[];
-    float(*red)[MT * 8][17] = reinterpret_cast<float(*)[MT * 8][17]>(gv_smem);  // [2 WARPS]
-    float *xsum = reinterpret_cast<float *>(gv_smem + gv_red_bytes(MT, WARPS));  // [k / 128][MT * 8]
+    float(*red)[MT * 8][ROWS + 1] = reinterpret_cast<float(*)[MT * 8][ROWS + 1]>(gv_smem);  // [2 WARPS]
+    float *xsum = reinterpret_cast<float *>(gv_smem + gv_red_bytes(MT, RT, WARPS));  // [k / 128][MT * 8]
     float *xshort = xsum + MT * 8 * (min(a.k_stage, a.K) >> 7);                  // the same
     uint4 *xs = reinterpret_cast<uint4 *>(xshort + MT * 8 * (min(a.k_stage, a.K) >> 7));  // [k / 128][word][M][t]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = a.split, wk = warp % split, wn = warp / split, per_cta = WARPS / split;
-    const int groups = a.K >> 7, row_tiles = (a.N + 15) >> 4, cta_tiles = (row_tiles + per_cta - 1) / per_cta;
+    const int groups = a.K >> 7, row_tiles = (a.N + ROWS - 1) / ROWS, cta_tiles = (row_tiles + per_cta - 1) / per_cta;
     const size_t row_bytes = (size_t)a.K / 2;
 
     struct Item {
-        uint4 c0, c1;
-        float s0, s1;
-    } item[GV_DEPTH];
-    // Where this lane's codes and scales of a row tile lie (rows past the
-    // last are the last one), and how far its next group is.
-    const uint8_t *c0, *c1;
-    const float *s0, *s1;
+        uint4 c[2 * RT];
+        float s[2 * RT];
+    } item[DEPTH];
+    // Where this lane's codes and scales of a row tile lie, rows g, g + 8, ...
+    // (rows past the last are the last one), and how far its next group is.
+    const uint8_t *code[2 * RT];
+    const float *scale[2 * RT];
     const size_t c_step = (size_t)split * 64, s_step = (size_t)split * a.N;
     const auto point = [&](int tile, int kg) {
-        const long long n = (long long)(tile * per_cta + wn) * 16 + g;
-        const long long r0 = min(n, (long long)a.N - 1), r1 = min(n + 8, (long long)a.N - 1);
-        c0 = a.codes + r0 * row_bytes + kg * 64 + t * 16;
-        c1 = a.codes + r1 * row_bytes + kg * 64 + t * 16;
-        s0 = a.scales + (size_t)kg * a.N + r0;
-        s1 = a.scales + (size_t)kg * a.N + r1;
+        const long long n = (long long)(tile * per_cta + wn) * ROWS + g;
+#pragma unroll
+        for (int i = 0; i < 2 * RT; i++) {
+            const long long r = min(n + 8 * i, (long long)a.N - 1);
+            code[i] = a.codes + r * row_bytes + kg * 64 + t * 16;
+            scale[i] = a.scales + (size_t)kg * a.N + r;
+        }
     };
     const auto fetch = [&](Item &x) {
-        x.c0 = ldg_stream16(c0);
-        x.c1 = ldg_stream16(c1);
-        x.s0 = *s0;
-        x.s1 = *s1;
-        c0 += c_step, c1 += c_step, s0 += s_step, s1 += s_step;
+#pragma unroll
+        for (int i = 0; i < 2 * RT; i++) {
+            x.c[i] = ldg_stream16(code[i]);
+            x.s[i] = *scale[i];
+            code[i] += c_step, scale[i] += s_step;
+        }
     };
     // x for k of [k0, k0 + n), scaled, in pairs (x0, x4), (x1, x5) / 16, (x2,
     // x6), (x3, x7) / 16, and the groups' sums; a thread has 32 values of a row.
@@ -189,77 +197,96 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
     int col[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; mt++) col[mt] = min(mt * 8 + g, a.M - 1) * 4 + t;
-    float acc[MT][4];
+    float acc[RT][MT][4];
     const auto clear = [&] {
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.0f;
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) acc[r][mt][0] = acc[r][mt][1] = acc[r][mt][2] = acc[r][mt][3] = 0.0f;
     };
     // a group's products; at: the group's place in xs. The sums stay 2^(90 -
     // 133) of themselves until the end.
     const auto take = [&](const Item &x, int at) {
-        const uint32_t w0[4] = {x.c0.x, x.c0.y, x.c0.z, x.c0.w}, w1[4] = {x.c1.x, x.c1.y, x.c1.z, x.c1.w};
         const uint4 *xg = xs + (size_t)at * 16 * a.M;
-        float part[MT][4];
+        float part[RT][MT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; mt++) {
             const float2 b = *reinterpret_cast<const float2 *>(xsum + (at * MT + mt) * 8 + 2 * t);
-            part[mt][0] = part[mt][2] = b.x, part[mt][1] = part[mt][3] = b.y;
+#pragma unroll
+            for (int r = 0; r < RT; r++) {
+                part[r][mt][0] = part[r][mt][2] = b.x;
+                part[r][mt][1] = part[r][mt][3] = b.y;
+            }
         }
 #pragma unroll
         for (int w = 0; w < 4; w++) {
-            uint32_t p0[4], p1[4];
+            uint32_t c[2 * RT][4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                p0[j] = q4_pair(w0[w], j);
-                p1[j] = q4_pair(w1[w], j);
+            for (int i = 0; i < 2 * RT; i++) {
+                const uint32_t word = w == 0 ? x.c[i].x : w == 1 ? x.c[i].y : w == 2 ? x.c[i].z : x.c[i].w;
+#pragma unroll
+                for (int j = 0; j < 4; j++) c[i][j] = q4_pair(word, j);
             }
 #pragma unroll
             for (int mt = 0; mt < MT; mt++) {
                 // columns past the last row repeat it; nobody reads their sums
                 const uint4 xv = xg[w * a.M * 4 + col[mt]];
-                mma_16816_bf16(part[mt], p0[0], p1[0], p0[1], p1[1], xv.x, xv.y);
-                mma_16816_bf16(part[mt], p0[2], p1[2], p0[3], p1[3], xv.z, xv.w);
-            }
-        }
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
-            if (huge) {
-                const float2 f = *reinterpret_cast<const float2 *>(xshort + (at * MT + mt) * 8 + 2 * t);
-                part[mt][0] *= f.x, part[mt][1] *= f.y, part[mt][2] *= f.x, part[mt][3] *= f.y;
+                for (int r = 0; r < RT; r++)
+                    mma_16816_bf16(part[r][mt], c[2 * r][0], c[2 * r + 1][0], c[2 * r][1], c[2 * r + 1][1], xv.x, xv.y);
+#pragma unroll
+                for (int r = 0; r < RT; r++)
+                    mma_16816_bf16(part[r][mt], c[2 * r][2], c[2 * r + 1][2], c[2 * r][3], c[2 * r + 1][3], xv.z, xv.w);
             }
-            acc[mt][0] = fmaf(part[mt][0], x.s0, acc[mt][0]);
-            acc[mt][1] = fmaf(part[mt][1], x.s0, acc[mt][1]);
-            acc[mt][2] = fmaf(part[mt][2], x.s1, acc[mt][2]);
-            acc[mt][3] = fmaf(part[mt][3], x.s1, acc[mt][3]);
         }
+        if (huge)
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+                const float2 f = *reinterpret_cast<const float2 *>(xshort + (at * MT + mt) * 8 + 2 * t);
+#pragma unroll
+                for (int r = 0; r < RT; r++) {
+                    part[r][mt][0] *= f.x, part[r][mt][1] *= f.y, part[r][mt][2] *= f.x, part[r][mt][3] *= f.y;
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+                acc[r][mt][0] = fmaf(part[r][mt][0], x.s[2 * r], acc[r][mt][0]);
+                acc[r][mt][1] = fmaf(part[r][mt][1], x.s[2 * r], acc[r][mt][1]);
+                acc[r][mt][2] = fmaf(part[r][mt][2], x.s[2 * r + 1], acc[r][mt][2]);
+                acc[r][mt][3] = fmaf(part[r][mt][3], x.s[2 * r + 1], acc[r][mt][3]);
+            }
     };
     // The bias of this lane's column of the outputs (all its outputs of a tile
     // have the same), asked for when the tile begins.
     float bias = 0.0f;
     const auto begin = [&](int tile) {
-        const long long n = (long long)(tile * per_cta + wn) * 16 + (lane & 15);
+        const long long n = (long long)(tile * per_cta + wn) * ROWS + lane % ROWS;
         if (a.bias && tile < cta_tiles && n < a.N) bias = a.bias[n];
     };
     // The sums of the row tile's warps, who wait for one another alone, and the
     // epilogue. With two buffers one barrier a tile is enough.
     int buf = 0;
     const auto finish = [&](int tile) {
-        float(*mine)[17] = red[buf * WARPS + warp];
+        float(*mine)[ROWS + 1] = red[buf * WARPS + warp];
 #pragma unroll
-        for (int mt = 0; mt < MT; mt++) {
-            mine[mt * 8 + 2 * t][g] = acc[mt][0];
-            mine[mt * 8 + 2 * t + 1][g] = acc[mt][1];
-            mine[mt * 8 + 2 * t][g + 8] = acc[mt][2];
-            mine[mt * 8 + 2 * t + 1][g + 8] = acc[mt][3];
-        }
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int mt = 0; mt < MT; mt++) {
+                mine[mt * 8 + 2 * t][16 * r + g] = acc[r][mt][0];
+                mine[mt * 8 + 2 * t + 1][16 * r + g] = acc[r][mt][1];
+                mine[mt * 8 + 2 * t][16 * r + g + 8] = acc[r][mt][2];
+                mine[mt * 8 + 2 * t + 1][16 * r + g + 8] = acc[r][mt][3];
+            }
         if (split > 1)
             named_bar_sync(1 + wn, 32 * split);
         else
             __syncwarp();
-        const int r = lane & 15;
-        const long long n = (long long)(tile * per_cta + wn) * 16 + r;
+        const int r = lane % ROWS;
+        const long long n = (long long)(tile * per_cta + wn) * ROWS + r;
         if (n < a.N)
-            for (int m = wk * 2 + (lane >> 4); m < a.M; m += split * 2) {
+            for (int m = wk * (32 / ROWS) + lane / ROWS; m < a.M; m += split * (32 / ROWS)) {
                 float y = 0.0f;
                 for (int w = 0; w < split; w++) y += red[buf * WARPS + wn * split + w][m][r];
                 y = y * 0x1p43f + bias;
@@ -286,12 +313,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
                 __syncthreads();
                 stage(k0, 128 * n);
                 point(tile, (k0 >> 7) + wk);
-                for (int kg = wk; kg < n; kg += GV_DEPTH * split) {
+                for (int kg = wk; kg < n; kg += DEPTH * split) {
 #pragma unroll
-                    for (int d = 0; d < GV_DEPTH; d++)
+                    for (int d = 0; d < DEPTH; d++)
                         if (kg + d * split < n) fetch(item[d]);
 #pragma unroll
-                    for (int d = 0; d < GV_DEPTH; d++)
+                    for (int d = 0; d < DEPTH; d++)
                         if (kg + d * split < n) take(item[d], kg + d * split);
                 }
             }
@@ -312,12 +339,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArg
         };
         point(next_tile, wk);
 #pragma unroll
-        for (int d = 0; d < GV_DEPTH; d++) ask(item[d]);
+        for (int d = 0; d < DEPTH; d++) ask(item[d]);
         stage(0, a.K);
         int tile = blockIdx.x, kg = wk;
         while (tile < cta_tiles) {
 #pragma unroll
-            for (int d = 0; d < GV_DEPTH; d++) {
+            for (int d = 0; d < DEPTH; d++) {
                 if (tile >= cta_tiles) break;
                 take(item[d], kg);
                 ask(item[d]);

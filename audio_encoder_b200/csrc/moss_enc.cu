@@ -2605,48 +2605,53 @@ static cudaError_t kernel_attrs(const moss_enc *h, std::atomic<uint64_t> &done, 
     return e;
 }
 
-// Warps that share a row tile of gemv_q4: as few as fill the SMs' 16 warps each
-// in whole rounds (a round more for each warp that a tile is split over is
-// 3 % of it: the sums' way through shared memory). Of N and K only, so that
-// the order of the sums does not depend on the number of rows.
-static int gemv_split(int sms, int N, int K)
+// Rows of N that a warp of gemv_q4 takes at a time, in sixteens, and the warps
+// that share them: as few as fill the SMs' 16 warps each in whole rounds (a
+// round more for each warp that a tile is split over is 3 % of it: the sums'
+// way through shared memory; 32 rows at once take RT2_COST of twice 16). Of N
+// and K only, so that the order of the sums, which the split makes, does not
+// depend on the number of rows.
+static void gemv_shape(int sms, int N, int K, int *rt, int *split)
 {
-    const double tiles = (N + 15) / 16, warps = 16.0 * sms;
-    int best = 1;
-    double best_cost = 1e30;
-    for (int split = 1; split <= 8 && split <= K / 128; split *= 2) {
-        const double cost = std::ceil(tiles * split / warps) / split * (1.0 + 0.03 * split);
-        if (cost < best_cost) best = split, best_cost = cost;
-    }
-    return best;
+    constexpr double RT2_COST = 0.8;
+    const double warps = 16.0 * sms;
+    double best = 1e30;
+    for (int r = 1; r <= 2; r++)
+        for (int s = 1; s <= 8 && s <= K / 128; s *= 2) {
+            const double tiles = (N + 16 * r - 1) / (16 * r);
+            const double cost = std::ceil(tiles * s / warps) / s * (1.0 + 0.03 * s) * (r == 1 ? 1.0 : 2 * RT2_COST);
+            if (cost < best) *rt = r, *split = s, best = cost;
+        }
 }
 
-template <int MT, int WARPS, bool STAGED = false>
-static moss_enc_status gemv_launch(moss_enc *h, const GemvArgs &a, size_t smem)
+template <int MT, int RT, int WARPS, bool STAGED = false>
+static moss_enc_status gemv_launch(moss_enc *h, const GemvArgs &a)
 {
     static std::atomic<uint64_t> done{0};
-    CUDA_TRY(h, kernel_attrs(h, done, gemv_q4_kernel<MT, WARPS, STAGED>, SMEM_LIMIT, false));
+    CUDA_TRY(h, kernel_attrs(h, done, gemv_q4_kernel<MT, RT, WARPS, STAGED>, SMEM_LIMIT, false));
     const int per_cta = WARPS / a.split;
-    const int64_t tiles = ((int64_t)a.N + 15) / 16;
+    const int64_t tiles = ((int64_t)a.N + 16 * RT - 1) / (16 * RT);
     const int64_t ctas = std::min<int64_t>((tiles + per_cta - 1) / per_cta, (int64_t)h->num_sms * (16 / WARPS));
-    CUDA_TRY(h, launch_k(h, gemv_q4_kernel<MT, WARPS, STAGED>, dim3((unsigned)ctas), dim3(32 * WARPS), smem, a));
+    CUDA_TRY(h, launch_k(h, gemv_q4_kernel<MT, RT, WARPS, STAGED>, dim3((unsigned)ctas), dim3(32 * WARPS),
+                         gv_red_bytes(MT, RT, WARPS) + gv_x_bytes(MT, a.M, a.k_stage), a));
     return MOSS_ENC_OK;
 }
 
 // Two CTAs of 8 warps an SM while all of x fits half of its shared memory, one
 // of 16 warps otherwise, which takes x in stages when even that is too little
 // (whole rounds of the warps that share a tile, so no sum changes its order).
-template <int MT>
+template <int MT, int RT>
 static moss_enc_status gemv_run(moss_enc *h, GemvArgs a)
 {
     a.k_stage = a.K;
     const size_t x = gv_x_bytes(MT, a.M, a.K);
-    if (x + gv_red_bytes(MT, 8) <= SMEM_LIMIT / 2 - 1024) return gemv_launch<MT, 8>(h, a, x + gv_red_bytes(MT, 8));
-    const size_t room = SMEM_LIMIT - gv_red_bytes(MT, 16);
-    if (x <= room) return gemv_launch<MT, 16>(h, a, x + gv_red_bytes(MT, 16));
+    if (x + gv_red_bytes(MT, RT, 8) <= SMEM_LIMIT / 2 - 1024) return gemv_launch<MT, RT, 8>(h, a);
+    constexpr size_t room = SMEM_LIMIT - gv_red_bytes(MT, RT, 16);
+    if (x <= room) return gemv_launch<MT, RT, 16>(h, a);
+    static_assert(gv_x_bytes(MT, 8 * MT, 8 * 128) <= room, "a stage holds a round of eight warps at least");
     const int round = 128 * a.split;
     a.k_stage = (int)(room / gv_x_bytes(MT, a.M, round)) * round;
-    return gemv_launch<MT, 16, true>(h, a, gv_x_bytes(MT, a.M, a.k_stage) + gv_red_bytes(MT, 16));
+    return gemv_launch<MT, RT, 16, true>(h, a);
 }
 
 extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs,
@@ -2675,10 +2680,13 @@ extern "C" moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const vo
     DecodeCall call(h);
     Launch L(h, "gemv_q4", 2.0 * M * N * K, 0.5 * N * (double)K + 4.0 * N * (K / 128) + 2.0 * M * K +
                                                 (epilogue == GV_RESID_F32 ? 8.0 : wide ? 4.0 : 2.0) * M * N);
-    a.split = gemv_split(h->num_sms, N, K);
-    if (M <= 8) return gemv_run<1>(h, a);
-    if (M <= 16) return gemv_run<2>(h, a);
-    return gemv_run<4>(h, a);
+    int rt = 1;
+    gemv_shape(h->num_sms, N, K, &rt, &a.split);
+    // (more than 8 rows leave no registers for a second sixteen of N's: 16 rows
+    // x 131071 x 2048 took 66.7 us with it, 48.9 without)
+    if (M <= 8) return rt == 2 ? gemv_run<1, 2>(h, a) : gemv_run<1, 1>(h, a);
+    if (M <= 16) return gemv_run<2, 1>(h, a);
+    return gemv_run<4, 1>(h, a);
 }
 
 // The reasons for which the paged calls refuse their arguments (null: none);
