@@ -130,9 +130,10 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv)
 // of a turn (pos * inv_freq / 2 pi less its nearest whole number), and only
 // that fraction goes to fp32 for the sine and cosine.
 //
-// Bound by the memory. With one row a CTA every warp waited for positions,
-// page, angles and values in turn: 45000 rows of 16 + 8 + 8 heads x 128 took
-// 193 us (58 % of the copy rate); four rows keep 32 KB a CTA on the way.
+// Bound by the memory: 45000 rows of 16 + 8 + 8 heads x 128 take 121 us (93 %
+// of the copy rate), four rows a CTA keeping 32 KB of it on the way. With one
+// row a CTA every warp waited for positions, page, angles and values in turn
+// (193 us).
 template <typename T, bool E4M3, int ROWS>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
 {
@@ -356,9 +357,8 @@ __device__ __forceinline__ void row_pairs(const RawDims<BYTES> &a, const RawDims
 static constexpr int PA_WARPS = 8;
 
 // Positions that a warp takes in one step, in sixteens: as many as keep 8 KB
-// of the cache on its way per warp (128 KB an SM with 16 warps; an e4m3 cache
-// read 16 positions at a time had half of that and reached 53 % of the copy
-// rate).
+// of the cache on its way per warp (128 KB an SM with 16 warps; with half of
+// that for an e4m3 cache, 64 ragged sequences took 79 us, now 63).
 __host__ __device__ constexpr int pa_sub(int dim, bool e4m3) { return dim >= 256 ? 1 : (dim == 128 ? 1 : 2) * (e4m3 ? 2 : 1); }
 // Positions that the CTA's warps take at once.
 __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_WARPS * pa_sub(dim, e4m3); }
@@ -378,7 +378,10 @@ __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_W
 //
 // mma.sync rather than tcgen05: a tcgen05 product has 128 rows, and its
 // operands come from shared memory; here 8 columns suffice and the reads of
-// the cache are what bounds the kernel.
+// the cache are what bounds the kernel: 6.5 TB/s over 360000 positions of 8 key
+// heads x 128 in bf16, 5.4 TB/s in e4m3, where a step's work is longer. Going
+// through shared memory by cp.async to ask a step ahead took the former to 4.1
+// TB/s; holding two (smaller) steps in registers gained nothing in either.
 template <typename T, bool E4M3, int D, int NT>
 struct PagedState {
     static constexpr int KD = E4M3 ? 16 : 8;                 // dims in a lane's piece of a key row
@@ -715,7 +718,10 @@ __device__ __forceinline__ void warps_join(const S &st, float *slots, int warp, 
 // known on the device, so each CTA adds them up and takes an equal share of
 // the tiles. A share may end inside a unit (one sequence's key head); then the
 // unit's pieces go to the workspace and paged_join_kernel puts them together,
-// in the order of the positions, so results do not depend on timing.
+// in the order of the positions, so results do not depend on timing. 45000
+// positions of 8 key heads x 128: 39 us (580 with a CTA per unit), of which
+// the reads take 28; the rest is the way to the first read and the join.
+
 // Where a CTA's share starts.
 struct PagedShare {
     long long first, count;  // tiles

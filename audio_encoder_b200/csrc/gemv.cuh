@@ -80,7 +80,7 @@ __host__ __device__ constexpr size_t gv_red_bytes(int mt, int rt, int warps)
 // per group.
 __host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { return 2 * (size_t)M * k + mt * 64 * (size_t)(k / 128); }
 
-// Persistent CTAs of WARPS warps. A row tile is 16 rows of N; `split` warps
+// Persistent CTAs of WARPS warps. A row tile is 16 RT rows of N; `split` warps
 // share one, taking its groups of 128 k in turn, and add their sums in shared
 // memory; the CTA's WARPS / split row tiles make its tile.
 //
@@ -93,8 +93,15 @@ __host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { re
 // first-level cache instead, in its own order, used up that cache's rate: 8 x
 // 131071 x 2048 took 52.7 us.)
 //
-// The order of the sums depends on N and K alone, so a row of x gives the same
-// bits whatever other rows are with it.
+// What bounds it is the work per code, not the reads: these reads alone (16
+// rows x 64 bytes a warp and group) take 23 us for 131072 x 2048, as a copy
+// does, and the kernel takes 35.0 us for 8 rows (64 % of the copy rate) at one
+// instruction every second cycle. 32 rows a warp share what 8 rows of x cost
+// (37.2 us with 16); a queue in shared memory filled by cp.async (37.2), 24
+// warps an SM (38.5) and requests of 256 bytes a row (37.4) gained nothing.
+//
+// The order of the sums depends on N, K and the number of SMs alone, so a row
+// of x gives the same bits whatever other rows are with it.
 template <int MT, int RT, int WARPS, bool STAGED>
 __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) gemv_q4_kernel(GemvArgs a)
 {
