@@ -887,6 +887,39 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
     cluster_sync_all();  // nobody leaves while its slot is read
 }
 
+// One warp per unit, for many units of few positions, which leave most of a
+// CTA's warps without any: no joining at all.
+template <typename T, typename QT, bool E4M3, int D, int NT>
+__global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) paged_attn_warp_kernel(PagedAttnArgs a)
+{
+    using S = PagedState<T, E4M3, D, NT>;
+    const int lane = threadIdx.x & 31, units = a.c.hkv * a.head_groups;
+    const long long which = (long long)blockIdx.x * PA_WARPS + (threadIdx.x >> 5);
+    const int s = (int)(which / units), unit = (int)(which - (long long)s * units);
+    grid_dep_wait();
+    grid_dep_launch();
+    if (s >= a.c.n_seqs) return;
+    const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
+    const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
+    int page[S::SUB];
+    S::pages(a.c, s, 0, page);
+    const int len = paged_len(a, s, lane == 0);
+    S st;
+    st.clear();
+    st.template load_q<QT>(a.q + s * a.q_stride + (long long)h0 * D, heads, a.scale_log2 * (E4M3 ? a.c.k_scale : 1.0f), lane);
+    st.run(a.c, s, head, 0, 16 * S::SUB, len, page, lane);
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int i = 0; i < S::TILES; i++) {
+            PagedTile x;
+            x.o = make_float4(st.o[n][i][0], st.o[n][i][1], st.o[n][i][2], st.o[n][i][3]);
+            x.ml = make_float4(st.m[n][0], st.m[n][1], st.l[n][0], st.l[n][1]);
+            x.template store<S, QT>(a.out + ((long long)s * a.hq + h0) * D, a.lse ? a.lse + (long long)s * a.hq + h0 : nullptr, heads,
+                                    E4M3 ? a.c.v_scale : 1.0f, n, i, lane);
+        }
+}
+
 // CTA i joins the unit that was split from share i on: its first piece is the
 // share's second, the others are the first pieces of the next shares. A warp
 // has one tile and every PARTS-th piece. Which unit that is follows from

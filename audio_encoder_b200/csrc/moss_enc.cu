@@ -2853,18 +2853,23 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
 // The launch of paged_attn. A unit is a sequence's key head with up to 8 or 16
-// of its query heads; a cluster of `ways` CTAs takes one, or (split) the tiles
-// of all units are dealt out evenly, with a join after.
+// of its query heads; a warp takes one (ways 0), or a cluster of `ways` CTAs,
+// or (split) the tiles of all units are dealt out evenly, with a join after.
 //
-// Measured (us): a step, one tile per CTA, takes 1.05 or what its bytes take
-// at 6.6 TB/s; joining a cluster of 2..8 takes 1.1 and one of 16 takes 4; the
-// split's shares and join take 5. So a cluster is as large as its joining
-// pays for (1000 / 2000 / 4000 tokens, 8 key heads x 128, by 1, 2, 4, 8, 16
-// CTAs and split: 10.4, 8.4, 7.1, 5.5, 7.3, 9.3 / 17.8, 12.2, 9.0, 6.6, 7.3,
-// 10.1 / 33.7, 19.7, 12.9, 8.5, 9.3, 13.4). Only a bound on the lengths is
-// known here and clusters wait for the longest sequence, so past ATTN_STEPS
-// steps the split, which deals out the true lengths, is taken.
-constexpr int ATTN_STEPS = 8;
+// Measured (us): a step, one tile per CTA or sixteen positions of a warp, takes
+// 1.05 or what its bytes take at 6.6 TB/s; a CTA's start and end take 2.3, a
+// warp's on its own 3.4; joining a cluster of 2..8 takes 1.1 and one of 16
+// takes 4; the split's shares and join take 11. So a cluster is as large as its
+// joining pays for (1000 / 2000 / 4000 positions, 8 key heads x 128, by 1, 2,
+// 4, 8, 16 CTAs and split: 10.4, 8.4, 7.1, 5.5, 7.3, 9.3 / 17.8, 12.2, 9.0,
+// 6.6, 7.3, 10.1 / 33.7, 19.7, 12.9, 8.5, 9.3, 13.4), and a warp alone takes
+// what many short units there are (76 sequences of 0..47 positions, 16 key
+// heads: 10.0 by warps, 17.6 by CTAs, 19.9 split; 105 of 0..17, 10 key heads x
+// 256: 10.9, 32.3, 32.0; but 64 of 128, 8 key heads: 17.5, 10.8, 15.1). Only a
+// bound on the lengths is known here and clusters wait for the longest
+// sequence, so past ATTN_STEPS steps (ATTN_WARP_STEPS of a warp) the split,
+// which deals out the true lengths, is taken.
+constexpr int ATTN_STEPS = 8, ATTN_WARP_STEPS = 16;
 
 struct AttnGrid {
     int64_t ctas;
@@ -2886,11 +2891,15 @@ static AttnGrid attn_grid(const moss_enc *h, const moss_enc_kv_cache *c, int gro
     double best_us = 1e30;
     for (int ways = 1; ways <= 16 && ways <= tiles && (ways == 1 || units * ways <= resident); ways *= 2) {
         const double bytes = 2.0 * tile * c->head_dim * (e4m3 ? 1 : 2) * std::min<double>((double)units * ways, resident);
-        const double waves = std::max(1.0, (double)units * ways / resident);
-        const double us = (double)((tiles + ways - 1) / ways) * waves * std::max(1.05, bytes / 6.6e6) +
+        const double us = std::ceil((double)units * ways / resident) *
+                              (2.3 + (double)((tiles + ways - 1) / ways) * std::max(1.05, bytes / 6.6e6)) +
                           (ways == 1 ? 0.0 : ways <= 8 ? 1.1 : 4.0);
         if (us < best_us) best = ways, best_us = us;
     }
+    const int64_t steps = (bound * PA_WARPS + tile - 1) / tile;  // of a warp on its own
+    if (steps <= ATTN_WARP_STEPS &&
+        3.4 + (double)steps * 1.05 * std::ceil((double)units / ((double)resident * PA_WARPS)) < best_us)
+        return AttnGrid{(units + PA_WARPS - 1) / PA_WARPS, 0, false};
     if (tiles <= (int64_t)ATTN_STEPS * best && units * best <= INT32_MAX) return AttnGrid{units * best, best, false};
     return AttnGrid{std::min<int64_t>(units * tiles, resident), 1, true};
 }
@@ -2921,6 +2930,11 @@ static moss_enc_status paged_attn_run(moss_enc *h, const PagedAttnArgs &a, const
     constexpr size_t smem = sizeof(float) * S::SLOT * PA_WARPS, smem_ways = smem + sizeof(float) * S::SLOT;
     static_assert(smem_ways <= SMEM_LIMIT, "the warps' states fit shared memory");
     const dim3 grid((unsigned)g.ctas), block(32 * PA_WARPS);
+    if (g.ways == 0) {
+        Launch L(h, "paged_attn", flops, bytes);
+        CUDA_TRY(h, launch_k(h, paged_attn_warp_kernel<T, QT, E4M3, D, NT>, grid, block, 0, a));
+        return MOSS_ENC_OK;
+    }
     if (!g.split) {
         const auto kern = paged_attn_unit_kernel<T, QT, E4M3, D, NT>;
         static std::atomic<uint64_t> done{0};

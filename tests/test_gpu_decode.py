@@ -501,6 +501,19 @@ def test_paged_attn_many_sequences(enc, seqs):
     check_attn(enc, cache, randn((seqs, 6, 64), g, BF16, 2.0), lengths)
 
 
+@pytest.mark.parametrize("hq,hkv,dim,ct", [(50, 10, 256, F16), (48, 16, 128, BF16), (20, 20, 64, BF16), (36, 4, 128, E4M3),
+                                           (40, 2, 64, E4M3)])
+@pytest.mark.parametrize("longest", [1, 17, 60, 200])
+def test_paged_attn_many_short_sequences(enc, hq, hkv, dim, ct, longest):
+    g = gen(hq + longest)
+    seqs = 133
+    lengths = np.random.default_rng(longest).integers(0, longest + 1, seqs).tolist()
+    cache = make_cache(seqs, longest, 16, hkv, dim, ct, g, "head" if longest == 60 else "token")
+    q = randn((seqs, hq, dim), g, F16 if ct == F16 else BF16, 2.0)
+    check_attn(enc, cache, q, lengths)
+    check_attn(enc, cache, q, lengths, max_len=1)  # a bound below the lengths only sizes the launch
+
+
 def test_paged_attn_sharp_and_flat_scores(enc):
     g = gen(31)
     n = [777, 128, 4000]
