@@ -165,8 +165,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
         where[tid] = pos;
     }
 
+    // the grid's second dimension shares out the items of few, wide rows
     bool ready = false;
-    for (int it = tid;; it += blockDim.x) {
+    for (int it = blockIdx.y * blockDim.x + tid;; it += gridDim.y * blockDim.x) {
         const bool live = it < items;
         int h = it / per_head;
         const int j = it - h * per_head;

@@ -2833,10 +2833,16 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     Launch L(h, "kv_append", 3.0 * r->n_rows * r->rotary * (r->n_q_heads + cache->n_kv_heads),
              (double)r->n_rows * (4.0 * q_row + 2.0 * kv_row * (e4m3 ? 3 : 4) + 8.0));
     const int items = (r->n_q_heads + 2 * cache->n_kv_heads) * (cache->head_dim / 16);
-    const dim3 block(std::min(256, std::max(64, (items + 31) / 32 * 32)));
-    // four rows a CTA once that still gives every SM eight CTAs' worth
+    // a row's items in equal rounds of up to 256 threads
+    const int rounds = (items + 255) / 256;
+    const dim3 block(std::max(64, ((items + rounds - 1) / rounds + 31) / 32 * 32));
+    // Four rows a CTA once every SM has one (1200 rows of 60 heads x 64: 6.1 us,
+    // 7.1 a row each); rows wider than a CTA are shared by several while that
+    // leaves SMs with fewer than eight.
     const int rows = r->n_rows >= 4 * h->num_sms ? 4 : 1;
-    const dim3 grid((r->n_rows + rows - 1) / rows);
+    const int64_t ctas = ((int64_t)r->n_rows + rows - 1) / rows;
+    const int wide = (int)std::min<int64_t>((items + (int)block.x - 1) / (int)block.x, std::max<int64_t>(1, 8 * h->num_sms / ctas));
+    const dim3 grid((unsigned)ctas, (unsigned)std::min(wide, 65535));
     const bool b = r->dtype == MOSS_ENC_KV_BF16;
     void (*kern)(AppendArgs) =
         rows == 4 ? (b ? (e4m3 ? kv_append_kernel<bf16, true, 4> : kv_append_kernel<bf16, false, 4>)

@@ -278,6 +278,9 @@ APPENDS = [
     (13, 900, 64, 4, 2, 64, F16, F16, 64, True, "token"),
     (13, 901, 16, 3, 3, 128, BF16, E4M3, 64, False, "head"),
     (6, 2500, 256, 24, 4, 256, BF16, BF16, 256, False, "token"),
+    # few, wide rows
+    (1, 7, 16, 60, 10, 256, F16, E4M3, 16, False, "token"),
+    (3, 90, 32, 64, 16, 256, BF16, BF16, 128, True, "head"),
 ]
 
 
