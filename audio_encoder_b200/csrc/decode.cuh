@@ -265,6 +265,7 @@ struct PagedAttnArgs {
     long long q_stride;
     int hq, group;       // query heads, query heads per key head
     int head_groups;     // groups of 8 NT query heads that share a key head
+    bool few;            // up to 1024 sequences, whose tiles 32 bits count
     float scale_log2;    // scale * log2(e)
 };
 
@@ -720,7 +721,7 @@ __device__ __forceinline__ void warps_join(const S &st, float *slots, int warp, 
 // the tiles. A share may end inside a unit (one sequence's key head); then the
 // unit's pieces go to the workspace and paged_join_kernel puts them together,
 // in the order of the positions, so results do not depend on timing. 45000
-// positions of 8 key heads x 128: 39 us (580 with a CTA per unit), of which
+// positions of 8 key heads x 128: 38 us (580 with a CTA per unit), of which
 // the reads take 28; the rest is the way to the first read and the join.
 
 // Where a CTA's share starts.
@@ -739,14 +740,78 @@ __device__ __forceinline__ int paged_len(const PagedAttnArgs &a, int s, bool rep
     return min(max(len, 0), cap);
 }
 
+// x / y of whole numbers, in 32 bits where they fit (64-bit divisions are
+// long).
+__device__ __forceinline__ long long quotient(long long x, long long y)
+{
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+__device__ __forceinline__ PagedShare paged_part(long long total)
+{
+    PagedShare r;
+    r.share = max(quotient(total + gridDim.x - 1, gridDim.x), 1ll);
+    r.first = min(r.share * blockIdx.x, total);
+    r.count = min(r.share, total - r.first);
+    return r;
+}
+
+// Up to 1024 sequences, and tiles that 32 bits count: each warp by itself,
+// without a barrier. Lane i adds up the tiles of its span of the sequences; the
+// lanes then take one each of the span in which the share starts.
+template <int TILE>
+__device__ __forceinline__ PagedShare paged_share_warp(const PagedAttnArgs &a, int units)
+{
+    const int lane = threadIdx.x & 31, span = (a.c.n_seqs + 31) >> 5;
+    const bool report = blockIdx.x == 0 && threadIdx.x < 32;
+    const auto scan = [&](int v) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+            if (lane >= d) v += o;
+        }
+        return v;
+    };
+    const auto tiles = [&](int s, bool say) {
+        return s < a.c.n_seqs ? (paged_len(a, s, say) + TILE - 1) / TILE * units : 0;
+    };
+    PagedShare r;
+    if (a.c.n_seqs == 1) {
+        r = paged_part(tiles(0, report));
+        r.s = 0;
+        r.offset = r.first;
+        return r;
+    }
+    int mine = 0;
+    for (int i = 0; i < span; i++) mine += tiles(lane * span + i, report);
+    const int upto = scan(mine);
+    r = paged_part(__shfl_sync(0xFFFFFFFFu, upto, 31));
+    r.s = a.c.n_seqs;
+    r.offset = 0;
+    const unsigned past = __ballot_sync(0xFFFFFFFFu, upto > r.first);
+    if (r.count <= 0 || past == 0) return r;
+    const int from = __ffs(past) - 1, before = __shfl_sync(0xFFFFFFFFu, upto - mine, from);
+    if (span == 1) {
+        r.s = from;
+        r.offset = r.first - before;
+        return r;
+    }
+    const int one = lane < span ? tiles(from * span + lane, false) : 0, end = before + scan(one);
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, end > r.first)) - 1;
+    if (at < 0) return r;
+    r.s = from * span + at;
+    r.offset = r.first - __shfl_sync(0xFFFFFFFFu, end - one, at);
+    return r;
+}
+
 // Thread i of the CTA's WARPS warps adds up the tiles of its span of the
 // sequences; a scan over the spans gives the total and the span in which this
 // CTA's share starts, whose thread walks it.
 template <int TILE, int WARPS>
 __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int units)
 {
-    __shared__ long long warp_sums[WARPS];
-    __shared__ long long found[2];
+    if (a.few) return paged_share_warp<TILE>(a, units);
+    __shared__ long long warp_sums[WARPS], found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int span = (a.c.n_seqs + 32 * WARPS - 1) / (32 * WARPS);
     const int lo = min(tid * span, a.c.n_seqs), hi = min(lo + span, a.c.n_seqs);
@@ -767,10 +832,7 @@ __device__ __forceinline__ PagedShare paged_share(const PagedAttnArgs &a, int un
         if (w < warp) before += warp_sums[w];
         total += warp_sums[w];
     }
-    PagedShare r;
-    r.share = max((total + gridDim.x - 1) / gridDim.x, 1ll);
-    r.first = min(r.share * blockIdx.x, total);
-    r.count = min(r.share, total - r.first);
+    PagedShare r = paged_part(total);
     long long at = before + upto - mine;
     if (r.count > 0 && at <= r.first && r.first < at + mine) {
         for (int s = lo; s < hi; s++) {
@@ -812,7 +874,7 @@ __global__ void __launch_bounds__(32 * PA_WARPS, D <= 128 && NT == 1 ? 2 : 1) pa
     for (int s = sh.s; sh.count > 0 && s < a.c.n_seqs; s++, sh.offset = 0) {
         const int len = paged_len(a, s, false), tiles = (len + S::TILE - 1) / S::TILE;
         if (tiles == 0) continue;
-        int unit = (int)(sh.offset / tiles), tile = (int)(sh.offset - (long long)unit * tiles);
+        int unit = (int)quotient(sh.offset, tiles), tile = (int)(sh.offset - (long long)unit * tiles);
         for (; unit < units && sh.count > 0; unit++, tile = 0) {
             const int head = unit / a.head_groups, hg = unit - head * a.head_groups;
             const int h0 = head * a.group + hg * 8 * NT, heads = min(a.group - hg * 8 * NT, 8 * NT);
@@ -951,11 +1013,11 @@ __global__ void __launch_bounds__(2 * D * NT * pj_parts(D, NT)) paged_join_kerne
             end -= (long long)tiles * units;
             sh.offset -= (long long)tiles * units;
         }
-        unit = tiles > 0 ? (int)((end - 1) / tiles) : 0;
+        unit = tiles > 0 ? (int)quotient(end - 1, tiles) : 0;
         const long long starts = (long long)unit * tiles;
         if (starts >= sh.offset) left = starts + tiles - end;  // else it began in an earlier share
     }
-    const int more = (int)min((left + sh.share - 1) / sh.share, (long long)(gridDim.x - 1 - blockIdx.x));
+    const int more = left <= 0 ? 0 : (int)min(quotient(left + sh.share - 1, sh.share), (long long)(gridDim.x - 1 - blockIdx.x));
     grid_dep_wait();
     grid_dep_launch();
     if (more <= 0) return;

@@ -2836,8 +2836,8 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     // a row's items in equal rounds of up to 256 threads
     const int rounds = (items + 255) / 256;
     const dim3 block(std::max(64, ((items + rounds - 1) / rounds + 31) / 32 * 32));
-    // Four rows a CTA once every SM has one (1200 rows of 60 heads x 64: 6.1 us,
-    // 7.1 a row each); rows wider than a CTA are shared by several while that
+    // Four rows a CTA once every SM has one (1200 rows of 60 heads x 64: 6.1 us;
+    // with a row each 7.1); rows wider than a CTA are shared by several while that
     // leaves SMs with fewer than eight.
     const int rows = r->n_rows >= 4 * h->num_sms ? 4 : 1;
     const int64_t ctas = ((int64_t)r->n_rows + rows - 1) / rows;
@@ -2865,7 +2865,7 @@ static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 
 // Measured (us): a step, one tile per CTA or sixteen positions of a warp, takes
 // 1.05 or what its bytes take at 6.6 TB/s; a CTA's start and end take 2.3, a
 // warp's on its own 3.4; joining a cluster of 2..8 takes 1.1 and one of 16
-// takes 4; the split's shares and join take 11. So a cluster is as large as its
+// takes 4; the split's shares and join take 9. So a cluster is as large as its
 // joining pays for (1000 / 2000 / 4000 positions, 8 key heads x 128, by 1, 2,
 // 4, 8, 16 CTAs and split: 10.4, 8.4, 7.1, 5.5, 7.3, 9.3 / 17.8, 12.2, 9.0,
 // 6.6, 7.3, 10.1 / 33.7, 19.7, 12.9, 8.5, 9.3, 13.4), and a warp alone takes
@@ -2993,6 +2993,8 @@ extern "C" moss_enc_status moss_enc_paged_attn(moss_enc *h, const moss_enc_kv_ca
     const int columns = attn_columns(cache, a.group);
     a.head_groups = (a.group + 8 * columns - 1) / (8 * columns);
     a.scale_log2 = p->scale * 1.4426950408889634f;
+    a.few = cache->n_seqs <= 1024 && (double)cache->n_seqs * cache->n_kv_heads * a.head_groups *
+                                             ((double)cache->page_size * cache->pages_per_seq / 128 + 1) < 2e9;
     const AttnGrid g = attn_grid(h, cache, a.group, p->max_len);
     const int64_t need = attn_workspace(h, cache, a.group, p->max_len);
     if (need > 0 && (!p->workspace || !aligned(p->workspace, 16) || p->workspace_bytes < need))

@@ -488,7 +488,8 @@ def test_paged_attn_pages_and_layouts(enc, page, layout):
 
 @pytest.mark.parametrize("ct", [BF16, F16, E4M3])
 @pytest.mark.parametrize("lengths", [[1500], [9000], [45000], [20000, 3], [4097, 0, 4096, 4095, 1, 12345], [130000],
-                                     [0] * 70 + [9000, 0, 2500] + [1100] * 50])
+                                     [0] * 70 + [9000, 0, 2500] + [1100] * 50, [3] * 1100 + [20000] + [0, 5] * 40,
+                                     [0] * 33 + [30000]])
 def test_paged_attn_long(enc, ct, lengths):
     g = gen(sum(lengths))
     cache = make_cache(len(lengths), max(lengths), 64, 2, 128, ct, g)
