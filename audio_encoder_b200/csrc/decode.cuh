@@ -366,8 +366,16 @@ __host__ __device__ constexpr int pa_sub(int dim, bool e4m3) { return dim >= 256
 __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_WARPS * pa_sub(dim, e4m3); }
 
 // What a warp holds of up to 8 NT query heads that share a key head, over the
-// positions it has seen: with s = scale log2(e) q.k, the running maximum m,
-// l = sum 2^(s - m) and o = sum 2^(s - m) v.
+// positions it has seen: with s = scale log2(e) q.k, a reference m that follows
+// the running maximum, l = sum 2^(s - m) and o = sum 2^(s - m) v.
+//
+// The reference is the maximum itself where probabilities meet the values in
+// bf16, and 15 below it where they do in f16: with the largest at 2^15 (f16 ends
+// at 65504) a probability down to 2^-29 of it keeps all of f16's bits and one
+// down to 2^-39 some, instead of 2^-14 and 2^-24. Those that became zero would
+// stay in l and be missing from o: a loss of one sign, which grows with the
+// number of positions (up to 3 % of the largest's share with 2^20 of them below
+// 2^-25; below 2^-40, as it is now, 2^-20).
 //
 // Keys and values are the A operands, straight from global memory, and the
 // query heads are the 8 columns: S^T = K q^T has 16 positions x 8 heads, its
@@ -395,6 +403,7 @@ struct PagedState {
     static constexpr int ESZ = E4M3 ? 1 : 2;
     static constexpr int SUB = pa_sub(D, E4M3), TILE = pa_tile(D, E4M3);
     static constexpr int SLOT = NT * (TILES + 1) * 4 * 32;   // floats of a saved state
+    static constexpr int BELOW = std::is_same<T, __half>::value ? 15 : 0;  // how far m is below the maximum
 
     uint32_t q[NT][TILES][2];
     float o[NT][TILES][4];
@@ -411,6 +420,13 @@ struct PagedState {
 #pragma unroll
                 for (int j = 0; j < 4; j++) o[n][i][j] = 0.0f;
         }
+    }
+
+    // The reference for scores up to `top`. Past 2^23 subtracting could round to
+    // more than 2^16 times the largest probability, so there it is `top`.
+    __device__ __forceinline__ static float below(float top)
+    {
+        return BELOW == 0 || !(fabsf(top) < 0x1p23f) ? top : top - BELOW;
     }
 
     // The query heads as B operands; heads past `heads` are zero.  An e4m3
@@ -533,6 +549,7 @@ struct PagedState {
                 t0 = fmaxf(t0, __shfl_xor_sync(0xFFFFFFFFu, t0, x));
                 t1 = fmaxf(t1, __shfl_xor_sync(0xFFFFFFFFu, t1, x));
             }
+            t0 = below(t0), t1 = below(t1);
             if (__any_sync(0xFFFFFFFFu, t0 > m[n][0] || t1 > m[n][1])) {
                 const float n0 = fmaxf(m[n][0], t0), n1 = fmaxf(m[n][1], t1);
                 const float f0 = n0 == -INFINITY ? 1.0f : ex2_approx(m[n][0] - n0);
@@ -551,8 +568,9 @@ struct PagedState {
                 const float e2 = ex2_approx(s[u][n][2] - b0), e3 = ex2_approx(s[u][n][3] - b1);
                 l[n][0] += e0 + e2, l[n][1] += e1 + e3;
                 // the probabilities are rounded to the cache's 16-bit type
-                // for the product (half an ulp each, errors that average out
-                // over the positions); their sum keeps 32 bits
+                // for the product (at most half an ulp each, so that is what
+                // the outputs' relative error can come to); their sum keeps 32
+                // bits
                 pb[u][n][0] = movmatrix(from_f2<T>(e0, e1));
                 pb[u][n][1] = movmatrix(from_f2<T>(e2, e3));
             }
@@ -692,10 +710,13 @@ struct PagedTile {
         for (int e = 0; e < 2; e++) {
             const int h = n * 8 + 2 * t + e;
             if (h >= heads) continue;
-            const float l = e ? ml.w : ml.z, inv = l == 0.0f ? 0.0f : v_scale / l;
+            // in units of the maximum again (exactly), so that neither the
+            // logarithm nor v_scale / l loses bits to the reference
+            constexpr float DOWN = 1.0f / (1 << S::BELOW);
+            const float l = (e ? ml.w : ml.z) * DOWN, inv = l == 0.0f ? 0.0f : v_scale / l;
             *reinterpret_cast<uint32_t *>(out + (long long)h * S::DIM + d) =
-                from_f2<QT>((e ? o.y : o.x) * inv, (e ? o.w : o.z) * inv);
-            if (lse && g == 0 && i == 0) lse[h] = ((e ? ml.y : ml.x) + log2f(l)) * 0.69314718055994531f;
+                from_f2<QT>((e ? o.y : o.x) * DOWN * inv, (e ? o.w : o.z) * DOWN * inv);
+            if (lse && g == 0 && i == 0) lse[h] = ((e ? ml.y : ml.x) + S::BELOW + log2f(l)) * 0.69314718055994531f;
         }
     }
 };

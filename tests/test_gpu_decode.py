@@ -538,6 +538,62 @@ def test_paged_attn_sharp_and_flat_scores(enc):
         check_attn(enc, cache, q, n)
 
 
+@pytest.mark.parametrize("dt,ct", [(F16, F16), (BF16, E4M3), (F16, E4M3)])
+@pytest.mark.parametrize("lengths,max_len", [([16], 0), ([300, 0, 40], 0), ([5000], 0), ([131072], 0), ([9000, 16] * 80, 16)])
+def test_paged_attn_keeps_small_probabilities(enc, dt, ct, lengths, max_len):
+    # every 16th position scores 18 above the others and its value is zero, so
+    # the outputs are the others' alone: probabilities of 2^-26 of the largest
+    g = gen(70)
+    cache = make_cache(len(lengths), max(lengths), 16, 2, 64, ct, g)
+    byte = torch.uint8 if ct == E4M3 else ct
+    key, value = torch.zeros(2, 16, 2, 64, device="cuda")
+    key[0, :, 3] = 18.0
+    value[1:] = torch.linspace(2.0, 8.0, 64, device="cuda")
+    cache.k.view(byte)[:] = (key / cache.desc.k_scale).to(ct).view(byte)
+    cache.v.view(byte)[:] = (value / cache.desc.v_scale).to(ct).view(byte)
+    q = torch.zeros(len(lengths), 4, 64, dtype=dt, device="cuda")
+    q[..., 3] = 1.0
+    n = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    out, lse = enc.paged_attn(cache, q, n, 1.0, return_lse=True, max_len=max_len)
+    enc.synchronize()
+    ref, rlse, _, tlse = attn_ref(cache, q, lengths, 1.0)
+    # as attn_ref's bound, with the probabilities' rounding relative to each:
+    # a score to 18 * 2^-23 and the like, 2^-11 a probability
+    tol = ref.abs() * (half_step(F16) + 2 * (18 * U * 72 + 2.0 ** -21) + 4 * U * (n.double()[:, None, None] + 64))
+    within(out, ref, tol + (ref.abs() + tol) * half_step(dt) + TINY[dt], "out")
+    live = n > 0
+    within(lse[live], rlse[live], tlse[live], "lse")
+
+
+@pytest.mark.parametrize("dt,ct", [(BF16, BF16), (F16, F16), (BF16, E4M3), (F16, E4M3)])
+def test_paged_attn_very_large_scores_stay_finite(enc, dt, ct):
+    # every second position has the largest score, the others one far below:
+    # the outputs are the means of the former's values, whatever the score.
+    # Around 2^23 (5.81e6 log2(e)) 32 bits no longer tell a score less 15 from it
+    g = gen(76)
+    n = [1, 2, 15, 100, 3000]
+    cache = make_cache(5, 3000, 16, 2, 64, ct, g)
+    byte = torch.uint8 if ct == E4M3 else ct
+    key = torch.zeros(16, 2, 64, device="cuda")
+    key[0::2, :, 3], key[1::2, :, 3] = 8.0, -8.0
+    key[:, :, 4] = -16.0
+    cache.k.view(byte)[:] = (key / cache.desc.k_scale).to(ct).view(byte)
+    cache.v.view(byte)[:] = randn(cache.v.shape, g, ct, 1 / cache.desc.v_scale).view(byte)
+    lt = torch.tensor(n, dtype=torch.int32, device="cuda")
+    for top in (1e3, 5.7e6, 5.8145e6, 5.815e6, 5.9e6, 1.17e7, 1.2e7, 2.4e7, 5e7, 3e9, 1e30):
+        for below_zero in (0.0, 1.0):  # scores of top and -top, or of -top and -3 top
+            q = torch.zeros(5, 4, 64, dtype=dt, device="cuda")
+            q[..., 3], q[..., 4] = 1.0, below_zero
+            out, lse = enc.paged_attn(cache, q, lt, top / 8, return_lse=True)
+            enc.synchronize()
+            assert torch.isfinite(lse).all()
+            for s, count in enumerate(n):
+                v = read(cache, s, count)[1][0::2].repeat_interleave(2, 1)
+                ref = v.mean(0)
+                tol = v.abs().mean(0) * (half_step(ct if ct in (BF16, F16) else F16) + (count + 64) * 4 * U)
+                within(out[s], ref, tol + (ref.abs() + tol) * half_step(dt) + TINY[dt])
+
+
 def test_paged_attn_extreme_queries_over_an_e4m3_cache(enc):
     # bf16 queries outside f16's range, one head each; the products stay finite
     g = gen(33)
