@@ -52,6 +52,14 @@ struct PagedKV {
 
 // ------------------------------------------------------------ append
 
+// How rows come to the cache: as they are, as e4m3 over scales that are powers of
+// two (whose reciprocals are exact), or as e4m3 over any scales.
+enum : int { TO_OWN = 0, TO_E4M3_EXACT = 1, TO_E4M3 = 2 };
+
+struct E4m3Scale {
+    float scale, inv;
+};
+
 struct AppendArgs {
     PagedKV c;
     const uint16_t *k, *v, *q;
@@ -60,7 +68,7 @@ struct AppendArgs {
     const int *positions, *seqs;
     const double *inv_freq;
     int n_rows, hq, rotary, interleaved;
-    float inv_k_scale, inv_v_scale;
+    E4m3Scale k_scale, v_scale;
 };
 
 template <typename T>
@@ -107,17 +115,36 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
     return make_uint4(from_f2<T>(x[0], x[1]), from_f2<T>(x[2], x[3]), from_f2<T>(x[4], x[5]), from_f2<T>(x[6], x[7]));
 }
 
-// Eight values as e4m3 (round to nearest even, held at +-448; NaN stays NaN).
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv)
+// x / scale for a rounding to e4m3, as if it were rounded once. x * inv is within 2
+// ulp of the quotient; of the numbers whose last three bits are zero, all middles
+// between two e4m3 values among them, the nearest is within 6, so the sign of
+// what it leaves over (x - l * scale, of one multiply-add) says on which side of
+// it the quotient lies, and the result is that number or its neighbour there. What
+// is held at 448 anyway, and NaN, stays x * inv. (45000 rows of 16 + 8 + 8 heads x
+// 128 take 131 us, 116 over powers of two; with a division, which needs the same
+// step after it, 193.)
+__device__ __forceinline__ float over(float x, E4m3Scale s)
 {
-    uint32_t r[2];
+    const float p = x * s.inv;
+    const uint32_t l = (__float_as_uint(p) + 4) & ~7u;
+    const float left = fmaf(-__uint_as_float(l), s.scale, x);
+    const uint32_t by = left == 0.0f ? 0u : (uint32_t)((int)(__float_as_uint(left) ^ l) >> 31) | 1u;
+    return fabsf(p) < 512.0f ? __uint_as_float(l + by) : p;
+}
+
+// Eight values over their scale as e4m3 (round to nearest even, held at +-448;
+// NaN stays NaN).
+template <int TO>
+__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], E4m3Scale s)
+{
+    uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
-        r[i] = lo | (hi << 16);
+    for (int i = 0; i < 4; i++) {
+        const float2 y = TO == TO_E4M3_EXACT ? make_float2(x[2 * i] * s.inv, x[2 * i + 1] * s.inv)
+                                             : make_float2(over(x[2 * i], s), over(x[2 * i + 1], s));
+        r[i] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(r[0], r[1]);
+    return make_uint2(r[0] | (r[1] << 16), r[2] | (r[3] << 16));
 }
 
 // A CTA takes ROWS rows: an item is 16 values of each (values i .. i+7 and
@@ -134,7 +161,7 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv)
 // of the copy rate), four rows a CTA keeping 32 KB of it on the way. With one
 // row a CTA every warp waited for positions, page, angles and values in turn
 // (193 us).
-template <typename T, bool E4M3, int ROWS>
+template <typename T, int TO, int ROWS>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
 {
     // cosine and sine of pair f of each row at [f % 8][f / 8]: neighbouring
@@ -241,10 +268,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
                 *reinterpret_cast<uint4 *>(dst + d1) = pack8<T>(y);
             } else {
                 uint8_t *dst = (what == K ? a.c.k : a.c.v) + slot + h * a.c.stride_head;
-                if (E4M3) {
-                    const float inv = what == K ? a.inv_k_scale : a.inv_v_scale;
-                    *reinterpret_cast<uint2 *>(dst + d0) = pack8_e4m3(x, inv);
-                    *reinterpret_cast<uint2 *>(dst + d1) = pack8_e4m3(y, inv);
+                if constexpr (TO != TO_OWN) {
+                    const E4m3Scale s = what == K ? a.k_scale : a.v_scale;
+                    *reinterpret_cast<uint2 *>(dst + d0) = pack8_e4m3<TO>(x, s);
+                    *reinterpret_cast<uint2 *>(dst + d1) = pack8_e4m3<TO>(y, s);
                 } else {
                     *reinterpret_cast<uint4 *>(dst + 2 * d0) = pack8<T>(x);
                     *reinterpret_cast<uint4 *>(dst + 2 * d1) = pack8<T>(y);

@@ -2802,6 +2802,24 @@ static PagedKV paged_kv(const moss_enc *h, const moss_enc_kv_cache *c)
     return o;
 }
 
+static bool power_of_two(float x)
+{
+    int e;
+    return std::frexp(x, &e) == 0.5f;
+}
+
+// kv_append's kernel for rows of type T, `rows` of them a CTA.
+template <typename T>
+static auto append_kernel(int to, int rows)
+{
+    return rows == 4 ? (to == TO_OWN          ? kv_append_kernel<T, TO_OWN, 4>
+                        : to == TO_E4M3_EXACT ? kv_append_kernel<T, TO_E4M3_EXACT, 4>
+                                              : kv_append_kernel<T, TO_E4M3, 4>)
+                     : (to == TO_OWN          ? kv_append_kernel<T, TO_OWN, 1>
+                        : to == TO_E4M3_EXACT ? kv_append_kernel<T, TO_E4M3_EXACT, 1>
+                                              : kv_append_kernel<T, TO_E4M3, 1>);
+}
+
 extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, const moss_enc_kv_rows *r)
 {
     if (!h) return MOSS_ENC_ERR_INVALID_ARG;
@@ -2827,8 +2845,12 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     a.rotary = r->rotary;
     a.interleaved = r->interleaved;
     const bool e4m3 = cache->dtype == MOSS_ENC_KV_E4M3;
-    a.inv_k_scale = e4m3 ? 1.0f / cache->k_scale : 1.0f;
-    a.inv_v_scale = e4m3 ? 1.0f / cache->v_scale : 1.0f;
+    int to = TO_OWN;
+    if (e4m3) {
+        a.k_scale = E4m3Scale{cache->k_scale, 1.0f / cache->k_scale};
+        a.v_scale = E4m3Scale{cache->v_scale, 1.0f / cache->v_scale};
+        to = power_of_two(cache->k_scale) && power_of_two(cache->v_scale) ? TO_E4M3_EXACT : TO_E4M3;
+    }
     DecodeCall call(h);
     Launch L(h, "kv_append", 3.0 * r->n_rows * r->rotary * (r->n_q_heads + cache->n_kv_heads),
              (double)r->n_rows * (4.0 * q_row + 2.0 * kv_row * (e4m3 ? 3 : 4) + 8.0));
@@ -2843,12 +2865,7 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
     const int64_t ctas = ((int64_t)r->n_rows + rows - 1) / rows;
     const int wide = (int)std::min<int64_t>((items + (int)block.x - 1) / (int)block.x, std::max<int64_t>(1, 8 * h->num_sms / ctas));
     const dim3 grid((unsigned)ctas, (unsigned)std::min(wide, 65535));
-    const bool b = r->dtype == MOSS_ENC_KV_BF16;
-    void (*kern)(AppendArgs) =
-        rows == 4 ? (b ? (e4m3 ? kv_append_kernel<bf16, true, 4> : kv_append_kernel<bf16, false, 4>)
-                       : (e4m3 ? kv_append_kernel<__half, true, 4> : kv_append_kernel<__half, false, 4>))
-                  : (b ? (e4m3 ? kv_append_kernel<bf16, true, 1> : kv_append_kernel<bf16, false, 1>)
-                       : (e4m3 ? kv_append_kernel<__half, true, 1> : kv_append_kernel<__half, false, 1>));
+    const auto kern = r->dtype == MOSS_ENC_KV_BF16 ? append_kernel<bf16>(to, rows) : append_kernel<__half>(to, rows);
     CUDA_TRY(h, launch_k(h, kern, grid, block, 0, a));
     return MOSS_ENC_OK;
 }

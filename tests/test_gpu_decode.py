@@ -371,6 +371,26 @@ def test_kv_append_in_place_queries_and_special_values(enc):
     enc.synchronize()
 
 
+@pytest.mark.parametrize("k_scale,v_scale", [(0.1, 3.0), (129 / 21, 133 / 21), (1025 / 17, 1025 / 31), (1 / 192, 1031 / 23 / 1024),
+                                             (0.25, 4.0)])
+@pytest.mark.parametrize("dt", [BF16, F16])
+def test_kv_append_rounds_the_quotient_by_the_scale_once(enc, dt, k_scale, v_scale):
+    # every finite value of the type, as keys and as values; with 129 / 21 and the
+    # like 32 bits put quotients on the middle between two e4m3 values that are
+    # only near it
+    bits = torch.arange(1 << 16, device="cuda", dtype=torch.int32).to(torch.int16).view(dt)
+    x = torch.where(torch.isfinite(bits.float()), bits, torch.zeros((), dtype=dt, device="cuda")).view(512, 2, 64)
+    cache = make_cache(1, 512, 16, 2, 64, E4M3, gen(71), k_scale=k_scale, v_scale=v_scale)
+    pos = torch.arange(512, dtype=torch.int32, device="cuda")
+    enc.kv_append(cache, x, x.flip(0), pos, torch.zeros_like(pos))
+    enc.synchronize()
+    at = cache.page_table[0].long()[pos.long() // 16], pos.long() % 16
+    for pool, rows, scale in ((cache.k, x, cache.desc.k_scale), (cache.v, x.flip(0), cache.desc.v_scale)):
+        got = pool.view(torch.uint8)[at].view(E4M3).double()
+        bad = got != e4m3_64(rows.double() / scale)
+        assert not bad.any(), (int(bad.sum()), rows[bad][:4], got[bad][:4])
+
+
 def test_kv_append_reports_places_outside_the_cache(enc):
     g = gen(12)
     cache = make_cache(2, 32, 16, 2, 64, BF16, g)
