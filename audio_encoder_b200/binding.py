@@ -397,6 +397,12 @@ class Encoder:
             raise ValueError("x [M][1280] fp32, codes [M][640], sfa ceil(M/128)*20*512 bytes, g [M]")
         self._check(lib().moss_enc_nvf4_quant_rows(self.h, _ptr(x), _ptr(codes), _ptr(sfa), _ptr(g), M))
 
+    def _mine(self, cache):
+        """The cache, which has to be on the handle's device."""
+        if cache.device != self.device:
+            raise ValueError(f"the cache must be on the handle's device ({self.device}), not {cache.device}")
+        return cache
+
     def _done(self, r):
         if type(r) is int:  # a status
             self._check(r)
@@ -417,8 +423,8 @@ class Encoder:
         inv_freq, in pairs (i, i + r/2) or, interleaved, (2i, 2i + 1).  q
         [rows][heads][head_dim] is turned into q_out (made here when None; may
         be q).  Returns q_out."""
-        return self._done(pycalls().kv_append(self.hid, self.sid, self.device.index, cache.address, k, v, positions, seqs,
-                                              q, q_out, inv_freq, interleaved))
+        return self._done(pycalls().kv_append(self.hid, self.sid, self.device.index, self._mine(cache).address, k, v,
+                                              positions, seqs, q, q_out, inv_freq, interleaved))
 
     def paged_attn(self, cache, q, lengths, scale=None, out=None, lse=None, return_lse=False, max_len: int = 0,
                    workspace=None):
@@ -428,12 +434,12 @@ class Encoder:
         lengths (0: what the page table holds).  Returns out [n_seqs][heads]
         [head_dim], and the fp32 log-sum-exp [n_seqs][heads] with return_lse.
         workspace: uint8, paged_attn_workspace() bytes (made here when None)."""
-        return self._done(pycalls().paged_attn(self.hid, self.sid, self.device.index, cache.address, q, lengths, scale, out,
-                                               lse, return_lse, max_len, workspace))
+        return self._done(pycalls().paged_attn(self.hid, self.sid, self.device.index, self._mine(cache).address, q,
+                                               lengths, scale, out, lse, return_lse, max_len, workspace))
 
     def paged_attn_workspace(self, cache, heads: int, max_len: int = 0) -> int:
         """Bytes that paged_attn needs as workspace."""
-        need = int(lib().moss_enc_paged_attn_workspace(self.h, cache.ref, heads, int(max_len)))
+        need = int(lib().moss_enc_paged_attn_workspace(self.h, self._mine(cache).ref, heads, int(max_len)))
         if need < 0:
             raise MossEncError(1, "paged_attn: cache, heads or max_len refused")
         return need

@@ -1,6 +1,7 @@
 """What the paged-cache calls refuse (no GPU: moss_enc_paged_refusal is pure),
 and what the Python binding refuses before it calls the library."""
 import ctypes
+import types
 
 import pytest
 
@@ -137,3 +138,33 @@ def test_native_marshalling_refuses_what_is_not_on_the_gpu():
         m.paged_attn(0, 0, 0, ctypes.addressof(c), k, i, None, None, None, False, 0, None)
     with pytest.raises(TypeError):
         m.gemv_q4("handle", 0, 0, x, codes, scales, None, None, 0)
+
+
+class Calls:
+    """Stands in for the native calls (and the library): records each."""
+
+    def __init__(self, answer="done"):
+        self.made, self.answer = [], answer
+
+    def __getattr__(self, name):
+        return lambda *a: (self.made.append((name, a)), self.answer)[1]
+
+
+def encoder_on(device):
+    """An Encoder without a handle, for what it does before and after a call."""
+    e = object.__new__(binding.Encoder)
+    e.h, e.hid, e.sid, e.device, e.torch = None, 0, 0, torch.device("cuda", device), torch
+    return e
+
+
+def test_a_cache_on_another_device_is_refused(monkeypatch):
+    calls = Calls(-1)
+    monkeypatch.setattr(binding, "pycalls", lambda: calls)
+    monkeypatch.setattr(binding, "lib", lambda: calls)
+    e = encoder_on(0)
+    c = types.SimpleNamespace(device=torch.device("cuda", 1), address=P, ref=None)
+    for call in (lambda: e.kv_append(c, None, None, None), lambda: e.paged_attn(c, None, None),
+                 lambda: e.paged_attn_workspace(c, 8)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    assert not calls.made
