@@ -313,6 +313,7 @@ class Encoder:
         self.h = h
         self.hid, self.sid = h.value, stream.cuda_stream
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self.current_stream = torch._C._cuda_getCurrentRawStream
 
     def close(self):
         if getattr(self, "h", None):
@@ -403,9 +404,21 @@ class Encoder:
             raise ValueError(f"the cache must be on the handle's device ({self.device}), not {cache.device}")
         return cache
 
-    def _done(self, r):
+    def _done(self, r, *used):
+        """A call's answer, once it is enqueued.  Where torch's current stream is
+        not the handle's, the allocator is told of the other stream's use: of
+        what the call reads and writes on the handle's, so that the caller may
+        free it at once, and of what it made on the current one."""
         if type(r) is int:  # a status
             self._check(r)
+        if self.current_stream(self.device.index) != self.sid:
+            for t in used:
+                if t is not None:
+                    t.record_stream(self.stream)
+            if r is not None:
+                now = self.torch.cuda.current_stream(self.device)
+                for t in r if type(r) is tuple else (r,):
+                    t.record_stream(now)
         return r
 
     def gemv_q4(self, x, Bq, Bs, bias=None, out=None, epilogue: int = 0):
@@ -413,7 +426,8 @@ class Encoder:
         codes Bq [N][K/2] (uint8, even k in the low nibble, code q + 8) with
         group scales Bs [K/128][N] fp32; bias [N] fp32 or None.  Epilogues 0
         (bf16), 1 (GELU, bf16), 2 (fp32, out +=: give out) and 5 (fp32)."""
-        return self._done(pycalls().gemv_q4(self.hid, self.sid, self.device.index, x, Bq, Bs, bias, out, epilogue))
+        r = pycalls().gemv_q4(self.hid, self.sid, self.device.index, x, Bq, Bs, bias, out, epilogue)
+        return self._done(r, x, Bq, Bs, bias, out)
 
     def kv_append(self, cache, k, v, positions, seqs=None, q=None, q_out=None, inv_freq=None, interleaved=False):
         """Append rows to a KVCache: k, v [rows][n_kv_heads][head_dim], row r
@@ -423,8 +437,9 @@ class Encoder:
         inv_freq, in pairs (i, i + r/2) or, interleaved, (2i, 2i + 1).  q
         [rows][heads][head_dim] is turned into q_out (made here when None; may
         be q).  Returns q_out."""
-        return self._done(pycalls().kv_append(self.hid, self.sid, self.device.index, self._mine(cache).address, k, v,
-                                              positions, seqs, q, q_out, inv_freq, interleaved))
+        r = pycalls().kv_append(self.hid, self.sid, self.device.index, self._mine(cache).address, k, v, positions, seqs, q,
+                                q_out, inv_freq, interleaved)
+        return self._done(r, cache.k, cache.v, cache.page_table, k, v, positions, seqs, q, q_out, inv_freq)
 
     def paged_attn(self, cache, q, lengths, scale=None, out=None, lse=None, return_lse=False, max_len: int = 0,
                    workspace=None):
@@ -434,8 +449,9 @@ class Encoder:
         lengths (0: what the page table holds).  Returns out [n_seqs][heads]
         [head_dim], and the fp32 log-sum-exp [n_seqs][heads] with return_lse.
         workspace: uint8, paged_attn_workspace() bytes (made here when None)."""
-        return self._done(pycalls().paged_attn(self.hid, self.sid, self.device.index, self._mine(cache).address, q,
-                                               lengths, scale, out, lse, return_lse, max_len, workspace))
+        r = pycalls().paged_attn(self.hid, self.sid, self.device.index, self._mine(cache).address, q, lengths, scale, out,
+                                 lse, return_lse, max_len, workspace)
+        return self._done(r, cache.k, cache.v, cache.page_table, q, lengths, out, lse, workspace)
 
     def paged_attn_workspace(self, cache, heads: int, max_len: int = 0) -> int:
         """Bytes that paged_attn needs as workspace."""

@@ -168,3 +168,45 @@ def test_a_cache_on_another_device_is_refused(monkeypatch):
         with pytest.raises(ValueError, match="device"):
             call()
     assert not calls.made
+
+
+class Tensor:
+    """Stands in for a tensor: which streams its memory was said to be used on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+@pytest.mark.parametrize("same", [True, False])
+def test_memory_on_its_way_is_not_handed_out_again(monkeypatch, same):
+    # a handle on a stream of its own: what a call reads or writes may be freed
+    # by the caller as soon as it returns (a temporary always is), and what it
+    # made is used on the caller's stream
+    mine, callers = "the handle's stream", "the caller's stream"
+    e = encoder_on(0)
+    e.sid, e.stream, e.current_stream = 7, mine, lambda device: 7 if same else 8
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: callers)
+    made, lse = Tensor(), Tensor()
+    c = types.SimpleNamespace(device=e.device, address=P, k=Tensor(), v=Tensor(), page_table=Tensor())
+    pages = [c.k, c.v, c.page_table]
+
+    def check(answer, call, n):
+        calls = Calls(answer)
+        monkeypatch.setattr(binding, "pycalls", lambda: calls)
+        args = [Tensor() for _ in range(n)]
+        assert call(*args) is answer and len(calls.made) == 1
+        outs = [o for o in (answer if isinstance(answer, tuple) else (answer,)) if o is not None]
+        assert all(t.streams == ([] if same else [mine]) for t in args + pages * (calls.made[0][0] != "gemv_q4"))
+        assert all(t.streams == ([] if same else [callers]) for t in outs)
+        for t in args + pages + outs:
+            t.streams.clear()
+
+    check(made, lambda x, q, s, b: e.gemv_q4(x, q, s, b), 4)
+    check(made, lambda x, q, s, b, out: e.gemv_q4(x, q, s, b, out, 5), 5)
+    check(None, lambda k, v, p: e.kv_append(c, k, v, p), 3)
+    check(made, lambda k, v, p, s, q, o, i: e.kv_append(c, k, v, p, s, q, o, i, True), 7)
+    check(made, lambda q, n: e.paged_attn(c, q, n), 2)
+    check((made, lse), lambda q, n, o, l, w: e.paged_attn(c, q, n, None, o, l, True, 0, w), 5)

@@ -893,6 +893,43 @@ def test_decode_calls_on_a_stream_that_is_not_current():
     e.close()
 
 
+def test_decode_calls_on_another_stream_may_be_given_temporaries():
+    # the handle's stream is busy while the caller's goes on: what the calls
+    # were given is freed at once, and the next tensors of its size are NaN
+    g = gen(65)
+    e = binding.Encoder(weights(1), 1, max_samples=16000, max_clips=1)
+    cache, qkv, proj, inv, dims = step_setup(g, 3, 9000)
+    hq, hkv, dim, width = dims
+    n = torch.tensor([8000, 700, 1], dtype=torch.int32, device="cuda")
+    x = randn((3, width), g, BF16)
+
+    def ready(*made):  # on the current stream, before the handle's goes on
+        e.stream.wait_stream(torch.cuda.current_stream())
+        return made
+
+    def calls():
+        y = e.gemv_q4(*ready(x.clone()), *qkv)
+        q, k, v = (t.view(3, -1, dim) for t in y.split([hq * dim, hkv * dim, hkv * dim], 1))
+        q = e.kv_append(cache, k, v, *ready(n - 1, torch.arange(3, dtype=torch.int32, device="cuda"), q, None, inv.clone()))
+        o, lse = e.paged_attn(cache, q, *ready(n.clone()), return_lse=True)
+        return y, q, o, lse, e.gemv_q4(o.flatten(1), *ready(*(t.clone() for t in proj)), epilogue=5)
+
+    want = calls()
+    torch.cuda.synchronize()
+    sizes = [(t.shape, t.dtype) for t in (x, n, n.long(), inv, *proj)]
+    side = torch.cuda.Stream()
+    e.set_stream(side)
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)
+        got = calls()
+        junk = [torch.empty(s, dtype=t, device="cuda").view(torch.uint8).fill_(255) for s, t in sizes for _ in range(6)]
+        e.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del junk
+    e.close()
+
+
 def test_decode_calls_are_counted_and_profiled(enc):
     g = gen(63)
     cache, qkv, proj, inv, dims = step_setup(g, 3, 100)
