@@ -1466,13 +1466,15 @@ extern "C" moss_enc_status moss_enc_synchronize(moss_enc *h)
     CUDA_TRY(h, cudaStreamSynchronize(h->stream));
     int e[PAGE_FLAG_WORD + 1] = {};
     CUDA_TRY(h, cudaMemcpy(e, h->err, sizeof(e), cudaMemcpyDeviceToHost));
-    if (e[PAGE_FLAG_WORD] != 0) CUDA_TRY(h, cudaMemset(h->err + PAGE_FLAG_WORD, 0, sizeof(int)));
+    // one error a call: what is not reported yet stays for the next
     if (e[0] != 0) {
         CUDA_TRY(h, cudaMemset(h->err, 0, sizeof(int)));
         return fail(h, MOSS_ENC_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait timed out");
     }
-    if (e[PAGE_FLAG_WORD] != 0)
+    if (e[PAGE_FLAG_WORD] != 0) {
+        CUDA_TRY(h, cudaMemset(h->err + PAGE_FLAG_WORD, 0, sizeof(int)));
         return fail(h, MOSS_ENC_ERR_INVALID_ARG, "a sequence, position, length or page lies outside the paged cache");
+    }
     return MOSS_ENC_OK;
 }
 

@@ -197,7 +197,7 @@ moss_enc_status moss_enc_set_stream(moss_enc *h, void *stream);
 /* Wait for the handle's stream; return MOSS_ENC_ERR_DEVICE_TIMEOUT if a kernel
  * reported a timed-out wait since the last call, or MOSS_ENC_ERR_INVALID_ARG if
  * one found a sequence, position, length or page outside a paged cache (and
- * clear the flags). */
+ * clear that flag: where there are both, the next call returns the latter). */
 moss_enc_status moss_enc_synchronize(moss_enc *h);
 
 /* Release a handle: synchronises its stream, then frees the weights, the

@@ -417,6 +417,20 @@ def test_kv_append_reports_places_outside_the_cache(enc):
     assert torch.equal(cache.k[good[0, 1].long(), 15], k[0])
 
 
+def test_synchronize_reports_a_page_error_behind_a_timeout(enc):
+    cache = make_cache(2, 32, 16, 2, 64, BF16, gen(73))
+    k = randn((2, 2, 64), gen(74), BF16)
+    enc.selftest_timeout(20)
+    enc.kv_append(cache, k, k, torch.tensor([5, 32], dtype=torch.int32, device="cuda"))
+    got = []
+    for _ in range(2):
+        with pytest.raises(binding.MossEncError) as e:
+            enc.synchronize()
+        got.append(e.value.status)
+    assert got == [5, 1]
+    enc.synchronize()
+
+
 def test_kv_append_nothing_and_refusals(enc):
     g = gen(13)
     cache = make_cache(2, 32, 16, 2, 64, BF16, g)
