@@ -2754,11 +2754,18 @@ static const char *rows_refusal(const moss_enc_kv_cache *c, const moss_enc_kv_ro
     return nullptr;
 }
 
+// What the launch and the workspace follow.
+static const char *attn_size_refusal(const moss_enc_kv_cache *c, int n_q_heads, int max_len)
+{
+    if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % c->n_kv_heads != 0 || max_len < 0)
+        return "n_q_heads must be a multiple of n_kv_heads, max_len not negative";
+    if ((int64_t)c->n_seqs * c->n_kv_heads * ((n_q_heads / c->n_kv_heads + 7) / 8) > INT32_MAX) return "too many sequences and heads";
+    return nullptr;
+}
+
 static const char *attn_refusal(const moss_enc_kv_cache *c, const moss_enc_attn *p)
 {
-    if ((int64_t)c->n_seqs * c->n_kv_heads * ((p->n_q_heads / c->n_kv_heads + 7) / 8) > INT32_MAX) return "too many sequences and heads";
-    if (p->n_q_heads < 1 || p->n_q_heads > 65535 || p->n_q_heads % c->n_kv_heads != 0 || p->max_len < 0)
-        return "n_q_heads must be a multiple of n_kv_heads, max_len not negative";
+    if (const char *why = attn_size_refusal(c, p->n_q_heads, p->max_len)) return why;
     if (!row_type_ok(c, p->dtype)) return "q must be of the cache's 16-bit type (either with an e4m3 cache)";
     if (!std::isfinite(p->scale)) return "scale must be finite";
     const int64_t q_row = (int64_t)p->n_q_heads * c->head_dim;
@@ -2943,7 +2950,7 @@ static int64_t attn_workspace(const moss_enc *h, const moss_enc_kv_cache *c, int
 
 extern "C" int64_t moss_enc_paged_attn_workspace(const moss_enc *h, const moss_enc_kv_cache *cache, int n_q_heads, int max_len)
 {
-    if (!h || cache_refusal(cache) || n_q_heads < 1 || n_q_heads % cache->n_kv_heads != 0 || max_len < 0) return -1;
+    if (!h || cache_refusal(cache) || attn_size_refusal(cache, n_q_heads, max_len)) return -1;
     return attn_workspace(h, cache, n_q_heads / cache->n_kv_heads, max_len);
 }
 

@@ -720,6 +720,14 @@ def test_paged_attn_refuses_a_workspace_that_is_too_small(enc):
     assert enc.paged_attn_workspace(n_short, 4) == 0 and enc.paged_attn_workspace(cache, 4, max_len=100) == 0
 
 
+def test_paged_workspace_of_refused_heads(enc):
+    cache = make_cache(2, 64, 16, 1, 64, BF16, gen(72))
+    assert enc.paged_attn_workspace(cache, 65535) >= 0
+    for heads in (65536, 0, -1, 1 << 30):
+        with pytest.raises(binding.MossEncError):
+            enc.paged_attn_workspace(cache, heads)
+
+
 def test_paged_attn_reports_lengths_and_pages_outside_the_cache(enc):
     g = gen(40)
     cache = make_cache(2, 64, 16, 1, 64, BF16, g)
