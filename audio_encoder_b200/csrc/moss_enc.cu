@@ -1466,13 +1466,14 @@ extern "C" moss_enc_status moss_enc_synchronize(moss_enc *h)
     CUDA_TRY(h, cudaStreamSynchronize(h->stream));
     int e[PAGE_FLAG_WORD + 1] = {};
     CUDA_TRY(h, cudaMemcpy(e, h->err, sizeof(e), cudaMemcpyDeviceToHost));
-    // one error a call: what is not reported yet stays for the next
+    // One error a call: what is not reported yet stays for the next. Cleared in
+    // the order of the handle's stream, so that no later kernel's word is lost.
     if (e[0] != 0) {
-        CUDA_TRY(h, cudaMemset(h->err, 0, sizeof(int)));
+        CUDA_TRY(h, cudaMemsetAsync(h->err, 0, sizeof(int), h->stream));
         return fail(h, MOSS_ENC_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait timed out");
     }
     if (e[PAGE_FLAG_WORD] != 0) {
-        CUDA_TRY(h, cudaMemset(h->err + PAGE_FLAG_WORD, 0, sizeof(int)));
+        CUDA_TRY(h, cudaMemsetAsync(h->err + PAGE_FLAG_WORD, 0, sizeof(int), h->stream));
         return fail(h, MOSS_ENC_ERR_INVALID_ARG, "a sequence, position, length or page lies outside the paged cache");
     }
     return MOSS_ENC_OK;

@@ -431,6 +431,26 @@ def test_synchronize_reports_a_page_error_behind_a_timeout(enc):
     enc.synchronize()
 
 
+def test_page_errors_in_a_row_on_a_stream_of_its_own_are_all_reported():
+    # the error word is cleared in the order of the handle's stream, which the
+    # default stream does not wait for
+    e = binding.Encoder(weights(1), 1, max_samples=16000, max_clips=1)
+    cache = make_cache(2, 32, 16, 2, 64, BF16, gen(77))
+    k = randn((2, 2, 64), gen(78), BF16)
+    bad, good = (torch.tensor([5, p], dtype=torch.int32, device="cuda") for p in (32, 31))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    e.set_stream(side)
+    for i in range(200):
+        e.kv_append(cache, k, k, bad if i % 3 else good)
+        if i % 3:
+            with pytest.raises(binding.MossEncError):
+                e.synchronize()
+        else:
+            e.synchronize()
+    e.close()
+
+
 def test_kv_append_nothing_and_refusals(enc):
     g = gen(13)
     cache = make_cache(2, 32, 16, 2, 64, BF16, g)
