@@ -1,13 +1,17 @@
 """Builds libmoss_enc.so (all CUDA kernels + the C ABI) for sm_100a with nvcc,
-and _pycalls.so (the Python side of the single-token calls) with g++.
+and, where PyTorch is installed, the Python side of the single-token calls with
+g++ against PyTorch's and Python's headers.
 
-Run from anywhere:  python -m audio_encoder_b200.build
+Run from anywhere:  python -m audio_encoder_b200.build [--force] [-v] [--lib]
+(--lib: the library alone, for callers of the C ABI; it needs nvcc only)
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -34,27 +38,30 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(s) <= t for s in sources())
 
 
+class PycallsError(RuntimeError):
+    """The library is built, the Python side of the single-token calls is not."""
+
+
 def build_pycalls(force: bool = False) -> str:
-    if not force and os.path.exists(PYCALLS_LIB) and \
-            all(os.path.getmtime(s) <= os.path.getmtime(PYCALLS_LIB) for s in (PYCALLS, HEADER)):
-        return PYCALLS_LIB
-    import sysconfig
     import torch
+    lib = PYCALLS_LIB
+    if not force and os.path.exists(lib) and \
+            all(os.path.getmtime(s) <= os.path.getmtime(lib) for s in (PYCALLS, HEADER)):
+        return lib
     t = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = PYCALLS_LIB + f".tmp{os.getpid()}"
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{t}/include",
            f"-I{t}/include/torch/csrc/api/include", f"-I{cuda}/include", f"-I{sysconfig.get_paths()['include']}",
            "-o", tmp, PYCALLS, f"-L{t}/lib", f"-Wl,-rpath,{t}/lib", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch", "-ltorch_python"]
     subprocess.run(cmd, check=True)
-    os.replace(tmp, PYCALLS_LIB)
-    return PYCALLS_LIB
+    os.replace(tmp, lib)
+    return lib
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_pycalls(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
@@ -69,6 +76,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
+def build(force: bool = False, verbose: bool = False) -> str:
+    """The library, and then the Python side of the single-token calls, whose
+    failure is a PycallsError. Without PyTorch that side has no user and is left
+    out."""
+    build_library(force, verbose)
+    if importlib.util.find_spec("torch") is None:
+        print("PyTorch is not installed: the Python side of the single-token calls is not built", file=sys.stderr)
+        return LIB
+    try:
+        build_pycalls(force)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
+        raise PycallsError(f"{LIB} is built, but not the Python side of the single-token calls: {e}") from e
+    return LIB
+
+
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    (build_library if "--lib" in sys.argv else build)(force="--force" in sys.argv, verbose="-v" in sys.argv)
     print(LIB)
