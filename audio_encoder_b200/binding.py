@@ -13,7 +13,6 @@ import numpy as np
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoss_enc.so")
-PYCALLS_PATH = os.path.join(HERE, "_pycalls.so")
 
 OK = 0
 STATUS = {0: "ok", 1: "invalid argument", 2: "capacity", 3: "out of memory", 4: "cuda error",
@@ -187,10 +186,11 @@ def pycalls():
     if _pycalls is None:
         import importlib.util
 
-        import torch  # noqa: F401  (its libraries first)
-        if not os.path.exists(PYCALLS_PATH):
-            raise ImportError(f"{PYCALLS_PATH} is not built; run `python -m audio_encoder_b200.build`")
-        spec = importlib.util.spec_from_file_location("audio_encoder_b200._pycalls", PYCALLS_PATH)
+        from . import build
+        path = build.pycalls_path()  # (imports torch, whose libraries come first)
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built; run `python -m audio_encoder_b200.build`")
+        spec = importlib.util.spec_from_file_location("audio_encoder_b200._pycalls", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         L = lib()

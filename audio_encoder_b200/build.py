@@ -20,7 +20,6 @@ MAIN = os.path.join(SRC_DIR, "moss_enc.cu")
 LIB = os.path.join(HERE, "libmoss_enc.so")
 HEADER = os.path.join(ROOT, "include", "moss_enc.h")
 PYCALLS = os.path.join(SRC_DIR, "pycalls.cpp")
-PYCALLS_LIB = os.path.join(HERE, "_pycalls.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared"]
@@ -42,9 +41,16 @@ class PycallsError(RuntimeError):
     """The library is built, the Python side of the single-token calls is not."""
 
 
+def pycalls_path() -> str:
+    """Where the Python side of the single-token calls is built: it is bound to
+    the interpreter's ABI and to PyTorch's, so its name has both."""
+    import torch
+    return os.path.join(HERE, f"_pycalls.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
+
+
 def build_pycalls(force: bool = False) -> str:
     import torch
-    lib = PYCALLS_LIB
+    lib = pycalls_path()
     if not force and os.path.exists(lib) and \
             all(os.path.getmtime(s) <= os.path.getmtime(lib) for s in (PYCALLS, HEADER)):
         return lib

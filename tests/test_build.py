@@ -50,5 +50,23 @@ def test_the_python_side_fails_after_the_library_and_with_an_error_of_its_own(mo
     assert build.build() == build.LIB and len(compilers) == 3  # nothing to do
 
 
+def test_another_pytorch_or_python_needs_another_python_side(monkeypatch, compilers):
+    # it is bound to the ABI of both
+    torch = pytest.importorskip("torch")
+    build.build()
+    monkeypatch.setattr(torch, "__version__", "99.1")
+    build.build()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-999")
+    build.build()
+    assert [c for c in compilers if c != "nvcc"] == compilers[1:] and len(compilers) == 4
+    files = [f for f in os.listdir(build.HERE) if f.startswith("_pycalls")]
+    assert len(files) == 3 and any("99.1" in f and "cpython-999" in f for f in files)
+    monkeypatch.setattr(torch, "__version__", "99.2")
+    from audio_encoder_b200 import binding
+    monkeypatch.setattr(binding, "_pycalls", None)
+    with pytest.raises(ImportError, match="99.2"):
+        binding.pycalls()
+
+
 def test_the_library_alone(compilers):
     assert build.build_library() == build.LIB and compilers == ["nvcc"]
