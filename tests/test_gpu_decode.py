@@ -551,6 +551,18 @@ def test_paged_attn_long(enc, ct, lengths):
     check_attn(enc, cache, q, lengths)
 
 
+@pytest.mark.parametrize("ct", [BF16, F16, E4M3])
+@pytest.mark.parametrize("hq,hkv,dim", [(3, 1, 256), (20, 2, 256), (32, 2, 128), (40, 2, 64), (24, 2, 64), (4, 2, 64), (17, 1, 128)])
+@pytest.mark.parametrize("lengths", [[70000, 0, 3], [66000, 0, 12345, 1, 700]])
+def test_paged_attn_split_over_the_card(enc, hq, hkv, dim, ct, lengths):
+    # the split and its join at every head width, with one and two groups of
+    # eight query heads a pass and several passes a key head
+    g = gen(hq + dim)
+    cache = make_cache(len(lengths), max(lengths), 64, hkv, dim, ct, g)
+    assert enc.paged_attn_workspace(cache, hq) > 0  # not a CTA or a cluster per key head
+    check_attn(enc, cache, randn((len(lengths), hq, dim), g, F16 if ct == F16 else BF16, 2.0), lengths)
+
+
 @pytest.mark.parametrize("seqs", [1, 40, 300, 1500])
 def test_paged_attn_many_sequences(enc, seqs):
     g = gen(seqs)
