@@ -498,7 +498,9 @@ moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, 
  *  lse        device fp32 [n_seqs][n_q_heads]: log sum_p exp(scale * q . k), or
  *             NULL.
  *  lengths    device int32 [n_seqs]: positions to attend, the new token's own
- *             included.  0 gives zeros and -inf.
+ *             included.  0 gives zeros and -inf, and so do positions whose
+ *             scores are all -inf (keys that mask themselves); a score of NaN
+ *             or +inf makes its row NaN.
  *  n_q_heads  a multiple of the cache's n_kv_heads.
  *  max_len    a bound on the lengths that the caller knows (0: the table's
  *             pages_per_seq * page_size); it sizes the launch and the

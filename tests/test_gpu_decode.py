@@ -702,6 +702,37 @@ def test_paged_attn_nan_in_a_live_place_reaches_its_rows_alone(enc):
     assert torch.equal(bad, want)
 
 
+def test_paged_attn_live_scores_of_minus_infinity(enc):
+    # a row that its keys mask throughout is as one without positions
+    g = gen(75)
+    lengths = [1, 40, 700, 20000, 130]
+    for ct, dt in ((BF16, BF16), (F16, F16)):
+        for seqs, max_len in ((1, 0), (5, 0), (5, 16), (5, 1 << 20)):
+            cache = make_cache(seqs, 20000 if seqs > 1 else 1000, 16, 2, 64, ct, g)
+            cache.k[..., 5] = -math.inf
+            q = randn((seqs, 4, 64), g, dt).abs()
+            n = torch.tensor(lengths[:seqs], dtype=torch.int32, device="cuda")
+            out, lse = enc.paged_attn(cache, q, n, return_lse=True, max_len=max_len)
+            enc.synchronize()
+            assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_paged_attn_a_score_of_infinity_makes_its_row_nan(enc):
+    g = gen(79)
+    for ct, dt in ((BF16, BF16), (F16, F16)):
+        for seqs, longest, max_len in ((1, 100, 0), (2, 2000, 0), (2, 20000, 0), (2, 20000, 16)):
+            cache = make_cache(seqs, longest, 16, 2, 64, ct, g)
+            cache.k[cache.page_table[0, 2].long(), 7, 1, 5] = math.inf
+            q = randn((seqs, 4, 64), g, dt).abs()
+            n = torch.full((seqs,), longest, dtype=torch.int32, device="cuda")
+            out, lse = enc.paged_attn(cache, q, n, return_lse=True, max_len=max_len)
+            enc.synchronize()
+            want = torch.zeros(seqs, 4, dtype=torch.bool, device="cuda")
+            want[0, 2:] = True
+            assert torch.equal(torch.isnan(out).all(2), want) and torch.equal(torch.isnan(out).any(2), want)
+            assert torch.equal(torch.isnan(lse), want)
+
+
 def test_paged_attn_strided_queries_and_given_outputs(enc):
     g = gen(37)
     cache = make_cache(5, 64, 16, 2, 64, BF16, g)
