@@ -446,7 +446,8 @@ class Encoder:
         """One new token per sequence of a KVCache: q [n_seqs][heads][head_dim]
         attends positions 0 .. lengths - 1 (int32 [n_seqs]) of its sequence;
         scale defaults to 1 / sqrt(head_dim).  max_len: a known bound on the
-        lengths (0: what the page table holds).  Returns out [n_seqs][heads]
+        lengths (0: what the page table holds), which chooses the launch: give
+        it where the table holds much more.  Returns out [n_seqs][heads]
         [head_dim], and the fp32 log-sum-exp [n_seqs][heads] with return_lse.
         workspace: uint8, paged_attn_workspace() bytes (made here when None)."""
         r = pycalls().paged_attn(self.hid, self.sid, self.device.index, self._mine(cache).address, q, lengths, scale, out,

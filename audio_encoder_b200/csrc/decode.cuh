@@ -157,10 +157,10 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], E4m3Scale s)
 // of a turn (pos * inv_freq / 2 pi less its nearest whole number), and only
 // that fraction goes to fp32 for the sine and cosine.
 //
-// Bound by the memory: 45000 rows of 16 + 8 + 8 heads x 128 take 121 us (93 %
-// of the copy rate), four rows a CTA keeping 32 KB of it on the way. With one
-// row a CTA every warp waited for positions, page, angles and values in turn
-// (193 us).
+// Bound by the memory: 45000 rows of 16 + 8 + 8 heads x 128 take 121 us in a
+// graph (93 % of the copy rate; 127 call by call, 88 %), four rows a CTA keeping
+// 32 KB of it on the way. With one row a CTA every warp waited for positions,
+// page, angles and values in turn (193 us).
 template <typename T, int TO, int ROWS>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a)
 {

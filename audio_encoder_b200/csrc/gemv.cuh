@@ -9,20 +9,23 @@
 // 16 c * 2^-133), because the first two binades of a binary format are linear
 // in its bits. So a pair costs one AND and every second one half a shift, no
 // conversion and no subtraction (adding 128 to make normal numbers, and taking
-// 136 off, cost twice the integer instructions, which bounded the kernel: 45.4
-// us for 8 x 131071 x 2048). x is multiplied by 2^90 (and by 2^-4 where it
-// meets 16 c), which is exact and keeps the products normal in fp32, and a
-// group's sum starts from -8 times the group's sum of x:
+// 136 off, cost twice the integer instructions: 45.4 us for 8 x 131071 x 2048).
+// x is multiplied by 2^90 (and by 2^-4 where it meets 16 c), which is exact, and
+// a group's sum starts from -8 times the group's sum of x:
 //   sum (c - 8) x = -8 sum x + sum c x.
 // A group's sum is fp32, and its fp32 scale multiplies it once: nothing rounds
 // a weight (the 4-bit GEMM rounds q * s to bf16, because its tiles need bf16
-// operands). An infinity in a row of x makes that row NaN.
+// operands). What is held is 2^-43 of the products and sums until the end, so
+// they are normal fp32 numbers from 2^-83 on, and below it steps of 2^-106; the
+// sum of a group of x is held as it is, so it has to stay below 2^128. An
+// infinity in a row of x makes that row NaN.
 //
-// mma.sync m16n8k16 rather than tcgen05: the weights are A (16 rows of N),
-// the few rows of x are B (8 columns), and the codes go from registers into
-// the instruction.  tcgen05 would need 128 expanded rows in shared memory per
-// instruction, and the shared-memory writes and reads of expanded weights
-// (four times the codes' bytes) would cost more than the products.
+// mma.sync m16n8k16: the weights are A (16 rows of N), the few rows of x are B
+// (8 columns), and the codes go from registers into the instruction. tcgen05
+// takes 128 rows of N at a time, with the expanded codes (four times the codes'
+// bytes) in shared memory or in TMEM; the latter was not tried here, and could
+// serve 9 to 32 rows, where each sixteen rows of N now read all of x from shared
+// memory.
 #pragma once
 
 #include "common.cuh"
@@ -93,12 +96,13 @@ __host__ __device__ constexpr size_t gv_x_bytes(int mt, int M, long long k) { re
 // first-level cache instead, in its own order, used up that cache's rate: 8 x
 // 131071 x 2048 took 52.7 us.)
 //
-// What bounds it is the work per code, not the reads: these reads alone (16
-// rows x 64 bytes a warp and group) take 23 us for 131072 x 2048, as a copy
-// does, and the kernel takes 35.0 us for 8 rows (64 % of the copy rate) at one
-// instruction every second cycle. 32 rows a warp share what 8 rows of x cost
-// (37.2 us with 16); a queue in shared memory filled by cp.async (37.2), 24
-// warps an SM (38.5) and requests of 256 bytes a row (37.4) gained nothing.
+// The reads do not bound it: these reads alone (16 rows x 64 bytes a warp and
+// group) take 23 us for 131072 x 2048, as a copy does, and the kernel takes 35 us
+// for 8 rows (64 % of the copy rate). No unit is full either (49 % of the issue
+// slots, 23 % of the tensor pipe): 16 warps an SM wait for their loads and for one
+// instruction after the other. 32 rows a warp share what 8 rows of x cost (37.2
+// us with 16); a queue in shared memory filled by cp.async (37.2), 24 warps an SM
+// (38.5) and requests of 256 bytes a row (37.4) gained nothing.
 //
 // The order of the sums depends on N, K and the number of SMs alone, so a row
 // of x gives the same bits whatever other rows are with it.

@@ -2613,7 +2613,9 @@ static cudaError_t kernel_attrs(const moss_enc *h, std::atomic<uint64_t> &done, 
 // round more for each warp that a tile is split over is 3 % of it: the sums'
 // way through shared memory; 32 rows at once take RT2_COST of twice 16). Of N
 // and K only, so that the order of the sums, which the split makes, does not
-// depend on the number of rows.
+// depend on the number of rows: more than 8 rows of x run sixteens with the split
+// found here for either height. Groups count as if they divided by the split
+// (10 groups of K = 1280 by 8 warps are two rounds, not 1.25).
 static void gemv_shape(int sms, int N, int K, int *rt, int *split)
 {
     constexpr double RT2_COST = 0.8;
@@ -2882,7 +2884,7 @@ extern "C" moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cac
 
 // Query heads of one key head that a CTA takes at once: one or two of the
 // matrix instruction's 8 columns (two cost twice the registers, which
-// head_dim 256 does not leave).
+// head_dim 256 does not leave). More of them read the keys and values again.
 static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 8 && c->head_dim <= 128 ? 2 : 1; }
 
 // The launch of paged_attn. A unit is a sequence's key head with up to 8 or 16
@@ -2898,10 +2900,12 @@ static int attn_columns(const moss_enc_kv_cache *c, int group) { return group > 
 // 6.6, 7.3, 10.1 / 33.7, 19.7, 12.9, 8.5, 9.3, 13.4), and a warp alone takes
 // what many short units there are (76 sequences of 0..47 positions, 16 key
 // heads: 10.0 by warps, 17.6 by CTAs, 19.9 split; 105 of 0..17, 10 key heads x
-// 256: 10.9, 32.3, 32.0; but 64 of 128, 8 key heads: 17.5, 10.8, 15.1). Only a
+// 256: 10.6, 32.3, 32.0; but 64 of 128, 8 key heads: 17.5, 11.6, 15.1). Only a
 // bound on the lengths is known here and clusters wait for the longest
 // sequence, so past ATTN_STEPS steps (ATTN_WARP_STEPS of a warp) the split,
-// which deals out the true lengths, is taken.
+// which deals out the true lengths, is taken. Where the caller gives no bound it
+// is what the table holds: 16 sequences of 125..375 positions in tables for 1500
+// or 11250 take the split's 12.2 us, 8.2 in tables for 375 or with that bound.
 constexpr int ATTN_STEPS = 8, ATTN_WARP_STEPS = 16;
 
 struct AttnGrid {

@@ -5,7 +5,7 @@
 // These calls run for a few microseconds on the GPU and a decoding step makes
 // several per layer, so their way through Python counts: checked and marshalled
 // in Python with ctypes, as the other calls are, they took 13 to 18 us of the
-// host's time each, here 5 to 8.
+// host's time each, here about 4.
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>

@@ -416,10 +416,12 @@ moss_enc_status moss_enc_nvf4_quant_weights(const void *w, int n, int k, int par
  *             5 (fp32).
  * Any N >= 1; K % 128 == 0; x and Bq 16-byte aligned, Bs, bias and out aligned
  * to their elements.  The sums are fp32 (of code * x and of x apart, so their
- * error is relative to sum |x| (code + 8) Bs) and the scale multiplies a group's
- * sum, so no weight is rounded (moss_enc_gemm_q4 multiplies bf16(q * s)).  A row
- * of x gives the same bits whatever other rows are with it; NaN or an infinity
- * in it makes that row NaN. */
+ * error is relative to sum |x| (code + 8) Bs, with steps of 2^-106 a product,
+ * which tell below |x| or |x| Bs of 2^-83; a group's sum of |x| has to stay below
+ * 2^128) and the scale multiplies a group's sum, so no weight is rounded
+ * (moss_enc_gemm_q4 multiplies bf16(q * s)).  A row of x gives the same bits
+ * whatever other rows are with it; NaN or an infinity in it makes that row
+ * NaN. */
 #define MOSS_ENC_GEMV_MAX_ROWS 32
 moss_enc_status moss_enc_gemv_q4(moss_enc *h, const void *x, const void *Bq, const float *Bs, const float *bias,
                                  void *out, int M, int N, int K, int epilogue);
@@ -435,7 +437,8 @@ enum { MOSS_ENC_KV_BF16 = 0, MOSS_ENC_KV_F16 = 1, MOSS_ENC_KV_E4M3 = 2 };
  *             [position][head] or [head][position].
  *  page_table device int32 [n_seqs][pages_per_seq], rows table_stride apart:
  *             page i of a sequence holds its positions i * page_size ...
- *             Entries past a sequence's last position are not read.
+ *             All n_seqs * pages_per_seq entries have to be readable: those past
+ *             a sequence's last position may be read, but are not used.
  *  page_size  a power of two, 16 or more; n_pages >= 1; pages_per_seq >= 1 and
  *             pages_per_seq * page_size <= 2^30.
  *  head_dim   64, 128 or 256.
@@ -504,7 +507,9 @@ moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, 
  *  n_q_heads  a multiple of the cache's n_kv_heads.
  *  max_len    a bound on the lengths that the caller knows (0: the table's
  *             pages_per_seq * page_size); it sizes the launch and the
- *             workspace, and longer sequences are still attended in full.
+ *             workspace, and longer sequences are still attended in full.  Worth
+ *             giving where tables hold much more than the sequences: the launch
+ *             for long ones takes some 4 us more over short ones.
  *  workspace  device, at least moss_enc_paged_attn_workspace() bytes, 16-byte
  *             aligned (NULL when that is 0).  Nothing in it has to be set
  *             before the call or kept after it, but calls whose work may
