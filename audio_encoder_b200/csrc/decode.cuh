@@ -392,6 +392,17 @@ __host__ __device__ constexpr int pa_sub(int dim, bool e4m3) { return dim >= 256
 // Positions that the CTA's warps take at once.
 __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_WARPS * pa_sub(dim, e4m3); }
 
+// The largest 16-bit numbers below x and y (both positive, or 0, which stays).
+template <typename T>
+__device__ __forceinline__ uint32_t below_f2(float x, float y)
+{
+    const uint32_t a = __float_as_uint(x) - (x != 0.0f), b = __float_as_uint(y) - (y != 0.0f);
+    if constexpr (std::is_same<T, bf16>::value) return __byte_perm(a, b, 0x7632);
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(b)), "f"(__uint_as_float(a)));
+    return r;
+}
+
 // What a warp holds of up to 8 NT query heads that share a key head, over the
 // positions it has seen: with s = scale log2(e) q.k, a reference m that follows
 // the running maximum, l = sum 2^(s - m) and o = sum 2^(s - m) v.
@@ -399,19 +410,24 @@ __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_W
 // The reference is the maximum itself where probabilities meet the values in
 // bf16, and 15 below it where they do in f16: with the largest at 2^15 (f16 ends
 // at 65504) a probability down to 2^-29 of it keeps all of f16's bits and one
-// down to 2^-39 some, instead of 2^-14 and 2^-24. Those that became zero would
+// down to 2^-40 some, instead of 2^-14 and 2^-25. Those that became zero would
 // stay in l and be missing from o: a loss of one sign, which grows with the
 // number of positions (up to 3 % of the largest's share with 2^20 of them below
 // 2^-25; below 2^-40, as it is now, 2^-20).
 //
 // Keys and values are the A operands, straight from global memory, and the
 // query heads are the 8 columns: S^T = K q^T has 16 positions x 8 heads, its
-// probabilities turn into the B operand of O^T = V^T P^T by two 8 x 8
-// transposes, and nothing passes through shared memory.  Lane (g, t) reads
-// key rows g and g + 8 in 16-byte pieces; which dims share an instruction's k
-// is free as long as q uses the same ones.  It reads its piece g of the value
-// rows 2t, 2t + 1, 2t + 8, 2t + 9 and pairs the rows' 16-bit halves, which
-// gives the V^T operand with the dims in an order that only the store knows.
+// probabilities turn into the B operands of O^T = V^T P^T by 8 x 8 transposes,
+// and nothing passes through shared memory. P is the sum of two 16-bit numbers:
+// the largest below the fp32 probability and what that leaves of it, rounded. So
+// it is off by 2^-16 (bf16) or 2^-22 (f16) of itself, and neither part is zero or
+// negative, which an infinite value would make NaN. The product with the second
+// costs 1 to 2 % (45000 positions 37.2 -> 37.5 us, 64 ragged e4m3 sequences 62.7
+// -> 63.9). Lane (g, t) reads key rows g and g + 8 in 16-byte pieces; which dims
+// share an instruction's k is free as long as q uses the same ones.  It reads its
+// piece g of the value rows 2t, 2t + 1, 2t + 8, 2t + 9 and pairs the rows' 16-bit
+// halves, which gives the V^T operand with the dims in an order that only the
+// store knows.
 //
 // mma.sync rather than tcgen05: a tcgen05 product has 128 rows, and its
 // operands come from shared memory; here 8 columns suffice and the reads of
@@ -540,7 +556,7 @@ struct PagedState {
                 v[u][i][3].load(p + i * 8 * VD * ESZ + 9 * c.stride_token);
             }
         }
-        uint32_t pb[SUB][NT][2];
+        uint32_t pb[SUB][NT][2], pr[SUB][NT][2];  // the probabilities' two parts
         float s[SUB][NT][4];
 #pragma unroll
         for (int u = 0; u < SUB; u++) {
@@ -594,12 +610,12 @@ struct PagedState {
                 const float e0 = ex2_approx(s[u][n][0] - b0), e1 = ex2_approx(s[u][n][1] - b1);
                 const float e2 = ex2_approx(s[u][n][2] - b0), e3 = ex2_approx(s[u][n][3] - b1);
                 l[n][0] += e0 + e2, l[n][1] += e1 + e3;
-                // the probabilities are rounded to the cache's 16-bit type
-                // for the product (at most half an ulp each, so that is what
-                // the outputs' relative error can come to); their sum keeps 32
-                // bits
-                pb[u][n][0] = movmatrix(from_f2<T>(e0, e1));
-                pb[u][n][1] = movmatrix(from_f2<T>(e2, e3));
+                const uint32_t p0 = below_f2<T>(e0, e1), p1 = below_f2<T>(e2, e3);
+                const float2 f0 = to_f2<T>(p0), f1 = to_f2<T>(p1);
+                pb[u][n][0] = movmatrix(p0);
+                pb[u][n][1] = movmatrix(p1);
+                pr[u][n][0] = movmatrix(from_f2<T>(e0 - f0.x, e1 - f0.y));
+                pr[u][n][1] = movmatrix(from_f2<T>(e2 - f1.x, e3 - f1.y));
             }
         }
         if (p0 + 16 * SUB > end) {
@@ -622,7 +638,10 @@ struct PagedState {
                     row_pairs<E4M3>(v[u][i][0], v[u][i][1], j, a0, a1);
                     row_pairs<E4M3>(v[u][i][2], v[u][i][3], j, a2, a3);
 #pragma unroll
-                    for (int n = 0; n < NT; n++) mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[u][n][0], pb[u][n][1]);
+                    for (int n = 0; n < NT; n++) {
+                        mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pb[u][n][0], pb[u][n][1]);
+                        mma_16816(T(), o[n][i * VJ + j], a0, a1, a2, a3, pr[u][n][0], pr[u][n][1]);
+                    }
                 }
     }
 

@@ -492,8 +492,9 @@ moss_enc_status moss_enc_kv_append(moss_enc *h, const moss_enc_kv_cache *cache, 
 
 /* One new token per sequence of the cache:
  *   out[s][h] = sum_{p < lengths[s]} softmax_p(scale * q[s][h] . k[s][p][h']) v[s][p][h'],
- * h' = h / (n_q_heads / n_kv_heads), in fp32 (probabilities rounded to 16 bits
- * for the product with the values, their sum not).
+ * h' = h / (n_q_heads / n_kv_heads), in fp32 (for the product with the values
+ * each probability is the sum of two numbers of the cache's 16-bit type, f16
+ * for e4m3: 2^-16 of itself with bf16, 2^-22 with f16).
  *  q          device [n_seqs][n_q_heads][head_dim], rows q_stride elements
  *             apart; bf16 or f16 as dtype says, the cache's own type unless
  *             that is e4m3.  16-byte aligned, q_stride a multiple of 8.

@@ -632,6 +632,38 @@ def test_paged_attn_keeps_small_probabilities(enc, dt, ct, lengths, max_len):
 
 
 @pytest.mark.parametrize("dt,ct", [(BF16, BF16), (F16, F16), (BF16, E4M3), (F16, E4M3)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_paged_attn_probabilities_are_not_held_in_16_bits(enc, dt, ct, dim):
+    # values of +w and -w in turn: the outputs are small differences of the
+    # probabilities, which the outputs' own rounding does not hide
+    g = gen(80 + dim)
+    lengths = [2, 3, 8, 15, 16, 17, 33, 40]
+    cache = make_cache(len(lengths), 40, 16, 2, dim, ct, g)
+    w = randn((1, 1, 2, dim), g, ct, 1 / cache.desc.v_scale).float()
+    sign = 1.0 - 2.0 * (torch.arange(16, device="cuda") % 2).view(1, 16, 1, 1)
+    byte = torch.uint8 if ct == E4M3 else ct
+    cache.v.view(byte)[:] = (w * sign).expand(cache.v.shape).to(ct).view(byte)
+    q = randn((len(lengths), 6, dim), g, dt)
+    scale = 0.2 * dim ** -0.5
+    out = enc.paged_attn(cache, q, torch.tensor(lengths, dtype=torch.int32, device="cuda"), scale)
+    enc.synchronize()
+    half = half_step(F16 if ct in (F16, E4M3) else BF16)
+    for s, n in enumerate(lengths):
+        k, v = read(cache, s, n)
+        qs = q[s].double().view(2, 3, dim)
+        score = torch.einsum("hgd,nhd->hgn", qs, k) * scale
+        size = torch.einsum("hgd,nhd->hgn", qs.abs(), k.abs()) * scale
+        p = torch.softmax(score, 2)
+        ref = torch.einsum("hgn,nhd->hgd", p, v)
+        pv = torch.einsum("hgn,nhd->hgd", p, v.abs())
+        # as attn_ref's bound, but a probability's rounding is that of what a
+        # rounding to 16 bits leaves of it
+        d = (size * U * (dim + 4) + score.abs() * 4 * U).amax(2) + 2 * 2.0 ** -22
+        tol = pv * (half * half + 2 * d[..., None] + 4 * U * (n + 64))
+        within(out[s].view(2, 3, dim), ref, tol + (ref.abs() + tol) * half_step(dt) + TINY[dt])
+
+
+@pytest.mark.parametrize("dt,ct", [(BF16, BF16), (F16, F16), (BF16, E4M3), (F16, E4M3)])
 def test_paged_attn_very_large_scores_stay_finite(enc, dt, ct):
     # every second position has the largest score, the others one far below:
     # the outputs are the means of the former's values, whatever the score.
@@ -715,6 +747,23 @@ def test_paged_attn_live_scores_of_minus_infinity(enc):
             out, lse = enc.paged_attn(cache, q, n, return_lse=True, max_len=max_len)
             enc.synchronize()
             assert (out == 0).all() and (lse == -math.inf).all()
+
+
+def test_paged_attn_infinite_values_in_live_places(enc):
+    # a value of +-inf makes its dim +-inf, and no other
+    g = gen(81)
+    for ct, dt in ((BF16, BF16), (F16, F16)):
+        for seqs, longest, max_len in ((2, 1, 0), (2, 100, 0), (2, 2000, 0), (2, 20000, 0), (2, 20000, 16)):
+            cache = make_cache(seqs, longest, 16, 2, 64, ct, g)
+            cache.v[cache.page_table[0, 0].long(), 0, 1, 5] = math.inf
+            cache.v[cache.page_table[1, 0].long(), 0, 0, 60] = -math.inf
+            n = torch.full((seqs,), longest, dtype=torch.int32, device="cuda")
+            for size in (0.0, 1.0):  # equal probabilities, or any
+                out = enc.paged_attn(cache, randn((seqs, 4, 64), g, dt, size), n, max_len=max_len).float()
+                enc.synchronize()
+                want = torch.zeros_like(out)
+                want[0, 2:, 5], want[1, :2, 60] = math.inf, -math.inf
+                assert torch.equal(torch.where(torch.isfinite(out), 0.0, out), want)
 
 
 def test_paged_attn_a_score_of_infinity_makes_its_row_nan(enc):
