@@ -392,7 +392,7 @@ __host__ __device__ constexpr int pa_sub(int dim, bool e4m3) { return dim >= 256
 // Positions that the CTA's warps take at once.
 __host__ __device__ constexpr int pa_tile(int dim, bool e4m3) { return 16 * PA_WARPS * pa_sub(dim, e4m3); }
 
-// The largest 16-bit numbers below x and y (both positive, or 0, which stays).
+// The largest 16-bit numbers below x and y (positive, or 0 or NaN, which stay).
 template <typename T>
 __device__ __forceinline__ uint32_t below_f2(float x, float y)
 {
@@ -420,8 +420,9 @@ __device__ __forceinline__ uint32_t below_f2(float x, float y)
 // probabilities turn into the B operands of O^T = V^T P^T by 8 x 8 transposes,
 // and nothing passes through shared memory. P is the sum of two 16-bit numbers:
 // the largest below the fp32 probability and what that leaves of it, rounded. So
-// it is off by 2^-16 (bf16) or 2^-22 (f16) of itself, and neither part is zero or
-// negative, which an infinite value would make NaN. The product with the second
+// it is off by 2^-16 (bf16) or 2^-22 (f16) of itself, and neither part is negative
+// or, from 16 bits' smallest number on, zero, which an infinite value would make
+// NaN. The product with the second
 // costs 1 to 2 % (45000 positions 37.2 -> 37.5 us, 64 ragged e4m3 sequences 62.7
 // -> 63.9). Lane (g, t) reads key rows g and g + 8 in 16-byte pieces; which dims
 // share an instruction's k is free as long as q uses the same ones.  It reads its
@@ -430,8 +431,8 @@ __device__ __forceinline__ uint32_t below_f2(float x, float y)
 // store knows.
 //
 // mma.sync rather than tcgen05: a tcgen05 product has 128 rows, and its
-// operands come from shared memory; here 8 columns suffice and the reads of
-// the cache are what bounds the kernel: 6.5 TB/s over 360000 positions of 8 key
+// operands come from shared memory or TMEM; here they come straight from the
+// loads, 8 columns suffice, and the reads of the cache are what bounds the kernel: 6.5 TB/s over 360000 positions of 8 key
 // heads x 128 in bf16, 5.4 TB/s in e4m3, where a step's work is longer. Going
 // through shared memory by cp.async to ask a step ahead took the former to 4.1
 // TB/s; holding two (smaller) steps in registers gained nothing in either.
@@ -610,12 +611,12 @@ struct PagedState {
                 const float e0 = ex2_approx(s[u][n][0] - b0), e1 = ex2_approx(s[u][n][1] - b1);
                 const float e2 = ex2_approx(s[u][n][2] - b0), e3 = ex2_approx(s[u][n][3] - b1);
                 l[n][0] += e0 + e2, l[n][1] += e1 + e3;
-                const uint32_t p0 = below_f2<T>(e0, e1), p1 = below_f2<T>(e2, e3);
-                const float2 f0 = to_f2<T>(p0), f1 = to_f2<T>(p1);
-                pb[u][n][0] = movmatrix(p0);
-                pb[u][n][1] = movmatrix(p1);
-                pr[u][n][0] = movmatrix(from_f2<T>(e0 - f0.x, e1 - f0.y));
-                pr[u][n][1] = movmatrix(from_f2<T>(e2 - f1.x, e3 - f1.y));
+                const uint32_t lo = below_f2<T>(e0, e1), hi = below_f2<T>(e2, e3);
+                const float2 flo = to_f2<T>(lo), fhi = to_f2<T>(hi);
+                pb[u][n][0] = movmatrix(lo);
+                pb[u][n][1] = movmatrix(hi);
+                pr[u][n][0] = movmatrix(from_f2<T>(e0 - flo.x, e1 - flo.y));
+                pr[u][n][1] = movmatrix(from_f2<T>(e2 - fhi.x, e3 - fhi.y));
             }
         }
         if (p0 + 16 * SUB > end) {
