@@ -422,20 +422,20 @@ __device__ __forceinline__ uint32_t below_f2(float x, float y)
 // the largest below the fp32 probability and what that leaves of it, rounded. So
 // it is off by 2^-16 (bf16) or 2^-22 (f16) of itself, and neither part is negative
 // or, from 16 bits' smallest number on, zero, which an infinite value would make
-// NaN. The product with the second
-// costs 1 to 2 % (45000 positions 37.2 -> 37.5 us, 64 ragged e4m3 sequences 62.7
-// -> 63.9). Lane (g, t) reads key rows g and g + 8 in 16-byte pieces; which dims
-// share an instruction's k is free as long as q uses the same ones.  It reads its
-// piece g of the value rows 2t, 2t + 1, 2t + 8, 2t + 9 and pairs the rows' 16-bit
-// halves, which gives the V^T operand with the dims in an order that only the
-// store knows.
+// NaN. The product with the second costs 1 to 2 % (45000 positions 37.2 -> 37.5
+// us, 64 ragged e4m3 sequences 62.7 -> 63.9). Lane (g, t) reads key rows g and
+// g + 8 in 16-byte pieces; which dims share an instruction's k is free as long as
+// q uses the same ones.  It reads its piece g of the value rows 2t, 2t + 1,
+// 2t + 8, 2t + 9 and pairs the rows' 16-bit halves, which gives the V^T operand
+// with the dims in an order that only the store knows.
 //
 // mma.sync rather than tcgen05: a tcgen05 product has 128 rows, and its
 // operands come from shared memory or TMEM; here they come straight from the
-// loads, 8 columns suffice, and the reads of the cache are what bounds the kernel: 6.5 TB/s over 360000 positions of 8 key
-// heads x 128 in bf16, 5.4 TB/s in e4m3, where a step's work is longer. Going
-// through shared memory by cp.async to ask a step ahead took the former to 4.1
-// TB/s; holding two (smaller) steps in registers gained nothing in either.
+// loads, 8 columns suffice, and the reads of the cache are what bounds the
+// kernel: 6.5 TB/s over 360000 positions of 8 key heads x 128 in bf16, 5.4 TB/s
+// in e4m3, where a step's work is longer. Going through shared memory by cp.async
+// to ask a step ahead took the former to 4.1 TB/s; holding two (smaller) steps in
+// registers gained nothing in either.
 template <typename T, bool E4M3, int D, int NT>
 struct PagedState {
     static constexpr int KD = E4M3 ? 16 : 8;                 // dims in a lane's piece of a key row
